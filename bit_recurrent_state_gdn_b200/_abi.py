@@ -1,4 +1,4 @@
-"""ctypes declarations of libgdnq's C ABI (include/gdnq.h, gdnq_pw.h, gdnq_prefill.h). Loading fails loudly when the
+"""ctypes declarations of libgdnq's C ABI (include/gdnq.h, gdnq_pw.h, gdnq_prefill.h, gdnq_layer.h). Loading fails loudly when the
 library has not been built: there is no fallback path."""
 from __future__ import annotations
 
@@ -16,7 +16,15 @@ GDN_DTYPE_F32, GDN_DTYPE_BF16 = 0, 1
 GDN_MAX_COMPENSATORS = 16
 GDN_PW_MAX_WINDOW = 16
 
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1, 2
+GDN_SCALE_NONE, GDN_SCALE_COMPLEMENT, GDN_SCALE_SQRT = 0, 1, 2
+GDN_WEIGHT_HEAD, GDN_WEIGHT_CHANNEL = 0, 1
+GDN_SCAN_CHUNK = 64
+GDN_NORM_MAX_D = 8192
+GDN_CONV_MAX_K = 4
+
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 
@@ -61,6 +69,25 @@ class gdn_pw_sizes(ctypes.Structure):
     _fields_ = [(n, _sz) for n in PW_SIZE_FIELDS]
 
 
+class gdn_tokens(ctypes.Structure):
+    _fields_ = [("ptr", _vp), ("sb", _i64), ("sl", _i64), ("sh", _i64)]
+
+
+class gdn_scan_config(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("B", "H", "D", "scale", "act_dtype")]
+
+
+class gdn_norm_config(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("B", "H", "D", "center", "activation", "weight",
+                                    "act_dtype")] + [("eps", ctypes.c_float)]
+
+
+class gdn_conv_config(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("B", "H", "D", "K", "activation", "act_dtype")]
+
+
+_TK = ctypes.POINTER(gdn_tokens)
+_SC, _NC, _CC = (ctypes.POINTER(c) for c in (gdn_scan_config, gdn_norm_config, gdn_conv_config))
 _PWC, _PWS = ctypes.POINTER(gdn_pw_config), ctypes.POINTER(gdn_pw_state)
 
 # name -> (restype, argtypes); every symbol the headers under include/ declare
@@ -87,6 +114,16 @@ SIGNATURES = {
     "gdn_pw_materialize": (_i32, [_PWC, _PWS, _vp, _vp]),
     "gdn_prefill": (_i32, [ctypes.POINTER(gdn_config), _i32] + [_vp] * 8 + [_sz, _vp]),
     "gdn_prefill_workspace_bytes": (_sz, [ctypes.POINTER(gdn_config), _i32]),
+    "gdn_gated_scan": (_i32, [_SC, _i32, _TK, _TK, _TK] + [_vp] * 5),
+    "gdn_gated_scan_backward": (_i32, [_SC, _i32, _TK, _TK, _vp, _TK, _vp, _TK, _TK] + [_vp] * 3),
+    "gdn_group_norm": (_i32, [_NC, _i32, _TK, _vp, _vp, _TK, _TK, _vp, _vp]),
+    "gdn_group_norm_backward": (_i32, [_NC, _i32, _TK, _vp, _vp, _TK, _TK, _TK, _TK]
+                                + [_vp] * 4 + [_sz, _vp]),
+    "gdn_group_norm_backward_workspace_bytes": (_sz, [_NC, _i32]),
+    "gdn_short_conv": (_i32, [_CC, _i32, _TK, _vp, _vp, _vp, _TK, _vp, _vp, _vp]),
+    "gdn_short_conv_backward": (_i32, [_CC, _i32, _TK, _vp, _vp, _vp, _TK, _vp, _TK]
+                                + [_vp] * 5 + [_sz, _vp]),
+    "gdn_short_conv_backward_workspace_bytes": (_sz, [_CC, _i32]),
     "gdn_status_string": (ctypes.c_char_p, [_i32]),
     "gdn_last_error": (ctypes.c_char_p, []),
 }

@@ -21,7 +21,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdnq.so")
 SOURCES = ["api.cu", "window_int8.cu", "window_int4.cu", "window_mixed.cu", "window_int8_smooth.cu",
            "window_int4_smooth.cu", "baseline.cu",
-           "pw.cu", "prefill.cu"]
+           "pw.cu", "prefill.cu", "layer_api.cu", "scan.cu", "norm.cu", "conv.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -42,7 +42,7 @@ def _flags(ptxas_info: bool) -> list[str]:
 
 def _deps() -> list[str]:
     files = [os.path.join(CSRC, n) for n in os.listdir(CSRC)]
-    return files + [os.path.join(INCLUDE, n) for n in ("gdnq.h", "gdnq_pw.h", "gdnq_prefill.h")]
+    return files + [os.path.join(INCLUDE, n) for n in os.listdir(INCLUDE)]
 
 
 def _stale() -> bool:

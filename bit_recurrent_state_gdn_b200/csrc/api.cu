@@ -12,15 +12,18 @@
 #include "launch.h"
 #include "prefill_args.h"
 #include "pw_kernels.cuh"
+#include "status.h"
 #include "window_kernels.cuh"
 
 // Staging of gdn_decode_window_steps_host_fixed: one fixed array per device, reserved when the
 // module loads (no allocation at call time).
 static __device__ __align__(256) uint8_t g_fixed_staging[GDN_FIXED_STAGING_BYTES];
 
-namespace {
+static thread_local char g_last_error[512] = "";
 
-thread_local char g_last_error[512] = "";
+namespace gdnq {
+
+void clear_error() { g_last_error[0] = 0; }
 
 gdn_status fail(gdn_status st, const char* fmt, ...) {
   va_list ap;
@@ -34,13 +37,20 @@ gdn_status cuda_fail(cudaError_t e, const char* where) {
   return fail(GDN_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-
-gdn_status need_ptr(const void* p, const char* name, unsigned align = 16) {
+gdn_status need_ptr(const void* p, const char* name, unsigned align) {
   if (!p) return fail(GDN_ERR_INVALID_ARG, "%s is null", name);
   if ((reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0)
     return fail(GDN_ERR_INVALID_ARG, "%s is not %u-byte aligned", name, align);
   return GDN_OK;
 }
+
+}  // namespace gdnq
+
+using gdnq::cuda_fail;
+using gdnq::fail;
+using gdnq::need_ptr;
+
+namespace {
 
 int64_t heads_of(const gdn_config* c) { return (int64_t)c->B * (int64_t)c->H; }
 size_t act_size(const gdn_config* c) { return c->act_dtype == GDN_DTYPE_F32 ? 4 : 2; }

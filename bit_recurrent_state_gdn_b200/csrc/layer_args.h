@@ -1,0 +1,66 @@
+// Kernel arguments and launch interface of the operators around the recurrence (gdnq_layer.h).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "gdnq_layer.h"
+
+namespace gdnq {
+
+// A token array on the device: element (b, l, h, d) at p[b sb + l sl + h sh + d].
+struct Tok {
+  void* p;
+  int64_t sb, sl, sh;
+};
+
+struct ScanArgs {
+  Tok x, g, o;            // forward; the backward pass reads x and g
+  Tok grad_o, grad_x, grad_g;
+  const float* h0;        // forward: h0; backward: grad_hT
+  float* hT;              // forward: hT; backward: grad_h0
+  float* hist;            // written forward, read backward
+  const int32_t* lens;
+  int B, L, H, D, C;      // C = H D
+};
+
+struct NormArgs {
+  Tok x, z, y;
+  Tok grad_y, grad_x, grad_z;
+  const float* w;
+  const float* bias;
+  float* grad_w;
+  float* grad_bias;
+  float* partials;        // backward: workspace
+  const int32_t* lens;
+  float eps, inv_d;
+  int B, L, H, D;
+  int center, activation, per_channel;
+};
+
+struct ConvArgs {
+  Tok x, y;
+  Tok grad_y, grad_x;
+  const float* w;
+  const float* bias;
+  const void* state_in;
+  void* state_out;
+  const void* grad_state_out;
+  void* grad_state_in;
+  float* grad_w;
+  float* grad_bias;
+  float* partials;
+  const int32_t* lens;
+  int B, L, H, D, C, K;
+  int activation;
+};
+
+cudaError_t launch_scan(const ScanArgs& a, const gdn_scan_config& cfg, cudaStream_t st);
+cudaError_t launch_scan_backward(const ScanArgs& a, const gdn_scan_config& cfg, cudaStream_t st);
+cudaError_t launch_norm(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st);
+cudaError_t launch_norm_backward(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st);
+size_t norm_backward_workspace(const gdn_norm_config& cfg, int L);
+cudaError_t launch_conv(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st);
+cudaError_t launch_conv_backward(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st);
+size_t conv_backward_workspace(const gdn_conv_config& cfg, int L);
+
+}  // namespace gdnq
