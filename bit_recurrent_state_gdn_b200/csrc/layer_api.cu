@@ -22,6 +22,7 @@ struct Shape {
 gdn_status check_shape(int64_t B, int64_t L, int64_t H, int64_t D, int act_dtype) {
   if (B < 0 || H < 0) return fail(GDN_ERR_INVALID_ARG, "B=%lld, H=%lld must be >= 0", (long long)B, (long long)H);
   if (L < 0) return fail(GDN_ERR_INVALID_ARG, "L=%lld must be >= 0", (long long)L);
+  if (L > (int64_t)1 << 30) return fail(GDN_ERR_INVALID_ARG, "L=%lld exceeds 2^30", (long long)L);
   if (D < 1) return fail(GDN_ERR_INVALID_ARG, "D=%lld must be >= 1", (long long)D);
   if (H * D > (int64_t)1 << 30) return fail(GDN_ERR_INVALID_ARG, "H*D exceeds 2^30");
   if (B * H > INT32_MAX) return fail(GDN_ERR_INVALID_ARG, "B*H exceeds 2^31-1");
@@ -94,6 +95,13 @@ gdn_status check_scan(const gdn_scan_config* c, int32_t L, Shape* s) {
     return fail(GDN_ERR_INVALID_ARG, "scale=%d is not a gdn_input_scale", c->scale);
   *s = Shape{c->B, L, c->H, c->D};
   return GDN_OK;
+}
+
+cudaError_t launch_scan(const gdnq::ScanArgs& a, const gdn_scan_config* c, bool backward,
+                        gdn_stream_t stream) {
+  return c->act_dtype == GDN_DTYPE_F32
+             ? gdnq::launch_scan_f32(a, c->scale, backward, (cudaStream_t)stream)
+             : gdnq::launch_scan_bf16(a, c->scale, backward, (cudaStream_t)stream);
 }
 
 gdn_status check_norm(const gdn_norm_config* c, int32_t L, Shape* s) {
@@ -179,7 +187,7 @@ gdn_status gdn_gated_scan(const gdn_scan_config* cfg, int32_t L, const gdn_token
   a.x = tok(x), a.g = tok(g), a.o = tok(o);
   a.h0 = h0, a.hT = hT, a.hist = hist, a.lens = lens;
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D;
-  const cudaError_t err = gdnq::launch_scan(a, *cfg, (cudaStream_t)stream);
+  const cudaError_t err = launch_scan(a, cfg, false, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_gated_scan");
 }
 
@@ -218,7 +226,7 @@ gdn_status gdn_gated_scan_backward(const gdn_scan_config* cfg, int32_t L, const 
   a.grad_o = tok(grad_o), a.grad_x = tok(grad_x), a.grad_g = tok(grad_g);
   a.h0 = grad_hT, a.hT = grad_h0, a.hist = const_cast<float*>(hist), a.lens = lens;
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D;
-  const cudaError_t err = gdnq::launch_scan_backward(a, *cfg, (cudaStream_t)stream);
+  const cudaError_t err = launch_scan(a, cfg, true, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_gated_scan_backward");
 }
 

@@ -54,8 +54,9 @@ struct ConvArgs {
   int activation;
 };
 
-cudaError_t launch_scan(const ScanArgs& a, const gdn_scan_config& cfg, cudaStream_t st);
-cudaError_t launch_scan_backward(const ScanArgs& a, const gdn_scan_config& cfg, cudaStream_t st);
+// Forward or backward scan, by activation type; scale is a gdn_input_scale.
+cudaError_t launch_scan_f32(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
+cudaError_t launch_scan_bf16(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
 cudaError_t launch_norm(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st);
 cudaError_t launch_norm_backward(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st);
 size_t norm_backward_workspace(const gdn_norm_config& cfg, int L);

@@ -19,7 +19,7 @@
  *   - Activations (GDN_DTYPE_BF16 or GDN_DTYPE_F32) are rounded once, to nearest even, when they
  *     are stored; parameters, their gradients, log-gates and scan states are fp32, and all
  *     arithmetic is fp32. Results do not depend on the order in which CTAs run.
- *   - Sizes: H D <= 2^30, B H < 2^31, B H D <= 2^36; offsets inside arrays are 64-bit.
+ *   - Sizes: L <= 2^30, H D <= 2^30, B H < 2^31, B H D <= 2^36; offsets inside arrays are 64-bit.
  *   - Errors: GDN_ERR_INVALID_ARG for a null or misaligned pointer, a bad size, stride or enum
  *     value, or a workspace too small; GDN_ERR_UNSUPPORTED for a size that is not built;
  *     GDN_ERR_CUDA for a failed launch.

@@ -8,6 +8,9 @@ joins of spans)."""
 import torch
 
 U = 2.0 ** -24
+# The hardware's exponential returns zero for e^g below fp32's smallest normal number: what such a
+# gate multiplies is then lost, at most 2^-126 of it.
+FLUSH = 2.0 ** -126
 N_OPS = 24
 
 
@@ -56,7 +59,7 @@ def scan(x, g, h0, scale, lens=None):
         a, u = g[:, t].exp(), scan_factor(g[:, t], scale) * torch.where(m, x[:, t], 0.0)
         n_h, n_s = a * h + u, a * size + u.abs()
         h, size = torch.where(m, n_h, h), torch.where(m, n_s, size)
-        err = torch.where(m, a * err + N_OPS * U * n_s, err)
+        err = torch.where(m, a * err + N_OPS * U * n_s + FLUSH * before[:, t].abs(), err)
         o[:, t], errs[:, t] = h, err
     return o, h, before, errs, errs_before, err
 
@@ -86,9 +89,9 @@ def scan_backward(x, g, h0, do, dhT, scale, lens=None):
         k, ek = a * before[:, t] + ds * xt, a * err_before[:, t]
         mag = a * before[:, t].abs() + (ds * xt).abs()
         dg[:, t] = k * dh
-        e_dg[:, t] = mag * e + ek * n_s + N_OPS * U * mag * n_s
+        e_dg[:, t] = mag * e + ek * n_s + N_OPS * U * mag * n_s + FLUSH * before[:, t].abs() * n_s
         carry = torch.where(m, a * dh, carry)
-        size, err = torch.where(m, a * n_s, size), torch.where(m, a * e, err)
+        size, err = torch.where(m, a * n_s, size), torch.where(m, a * e + FLUSH * n_s, err)
     return dx, dg, carry, e_dx, e_dg, err + N_OPS * U * size
 
 

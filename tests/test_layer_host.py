@@ -61,6 +61,7 @@ def test_sizes_beyond_the_limits_are_refused(lib, op):
     assert call(lib, make(B=1 << 20, H=1 << 20)) == BAD    # B H >= 2^31
     assert call(lib, make(B=1 << 20, H=1 << 10, D=128)) == BAD  # B H D > 2^36
     assert call(lib, make(), L=-1) == BAD
+    assert call(lib, make(), L=(1 << 30) + 1) == BAD
     assert lib.gdn_gated_scan(None, 1, *[None] * 8) == BAD
     assert lib.gdn_group_norm(None, 1, *[None] * 7) == BAD
     assert lib.gdn_short_conv(None, 1, *[None] * 8) == BAD
