@@ -50,6 +50,8 @@ gdn_status check_tokens(const gdn_tokens* t, const char* name, const Shape& s, u
     if (d.stride < 0) return fail(GDN_ERR_INVALID_ARG, "%s has a negative stride", name);
     span += (double)(d.size - 1) * (double)d.stride;
   }
+  if (s.L > 1 && t->sl > (int64_t)1 << 27)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: tokens further than 2^27 elements apart are not built", name);
   if (span * elem > 4e18) return fail(GDN_ERR_INVALID_ARG, "%s spans too many bytes", name);
   if (!output) return GDN_OK;
   std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });

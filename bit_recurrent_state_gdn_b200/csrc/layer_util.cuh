@@ -19,6 +19,13 @@ __device__ __forceinline__ int64_t channel_offset(const Tok& t, int b, int h, in
   return (int64_t)b * t.sb + (int64_t)h * t.sh + d;
 }
 
+// 1 / sqrt(x) on the hardware path.
+__device__ __forceinline__ float rsqrt_hw(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float sigmoidf(float u) { return 1.0f / (1.0f + __expf(-u)); }
 
 }  // namespace gdnq

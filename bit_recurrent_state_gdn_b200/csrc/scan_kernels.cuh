@@ -17,280 +17,428 @@
 
 namespace gdnq {
 
-constexpr int kScanWarps = 8;  // of a CTA: kScanWarps / W groups, each with a slab of its own
-
+// A gate's terms for the two channels of a lane.
 struct Gate {
-  float a, s;  // e^g, s(g)
-  float r;     // what the slope takes: 1 / s of GDN_SCALE_SQRT
+  F2 a, s;  // e^g, s(g)
+  F2 r;     // 1 / s of GDN_SCALE_SQRT, 0 where s is 0 (backward pass)
 };
 
-// e^g - 1 and e^g. Near zero e^g - 1 = g p(g), p of degree 5 through the Chebyshev points of
+__device__ __forceinline__ F2 f2_all(float x) { return f2(x, x); }
+
+// e^g and 1 - e^g. Near zero e^g - 1 = g p(g), p of degree 5 through the Chebyshev points of
 // [-0.35, 0.35], off by at most 2.6e-8 of itself (half an fp32 step is 6.0e-8), so that neither
-// 1 - e^g nor a gate near one loses digits; elsewhere by the hardware's exponential.
-__device__ __forceinline__ void exp_and_m1(float g, float& a, float& e) {
-  float p = 0.0013934532180428505f;
-  p = fmaf(p, g, 0.008369861170649529f);
-  p = fmaf(p, g, 0.04166645556688309f);
-  p = fmaf(p, g, 0.1666649878025055f);
-  p = fmaf(p, g, 0.5f);
-  p = fmaf(p, g, 1.0f);
-  const float big = fast_exp(g);
-  const bool near = fabsf(g) <= 0.35f;
-  e = near ? p * g : big - 1.0f;
-  a = near ? 1.0f + e : big;
+// 1 - e^g nor a gate near one loses digits; elsewhere by the hardware's exponential, which takes
+// e^g below 2^-126 as zero.
+__device__ __forceinline__ void exp_and_rest(F2 g, F2& a, F2& m) {
+  F2 p = f2_all(-0.0013934532180428505f);
+  p = f2_fma(p, g, f2_all(-0.008369861170649529f));
+  p = f2_fma(p, g, f2_all(-0.04166645556688309f));
+  p = f2_fma(p, g, f2_all(-0.1666649878025055f));
+  p = f2_fma(p, g, f2_all(-0.5f));
+  p = f2_fma(p, g, f2_all(-1.0f));
+  p = f2_mul(p, g);
+  float g0, g1, y0, y1, p0, p1;
+  f2_get(g, g0, g1);
+  f2_get(f2_mul(g, f2_all(1.4426950408889634f)), y0, y1);
+  y0 = exp2_hw(y0);
+  y1 = exp2_hw(y1);
+  f2_get(p, p0, p1);
+  const bool near0 = fabsf(g0) <= 0.35f, near1 = fabsf(g1) <= 0.35f;
+  m = f2(near0 ? p0 : 1.0f - y0, near1 ? p1 : 1.0f - y1);
+  a = f2(near0 ? 1.0f - p0 : y0, near1 ? 1.0f - p1 : y1);
 }
 
-template <int SCALE>
-__device__ __forceinline__ Gate gate_of(float g) {
+template <int SCALE, bool BACKWARD = false>
+__device__ __forceinline__ Gate gate_of(F2 g) {
   Gate q;
-  float e;
-  exp_and_m1(g, q.a, e);
-  q.s = 1.0f;
-  q.r = 0.0f;
-  if constexpr (SCALE == GDN_SCALE_COMPLEMENT) q.s = -e;
+  F2 m;
+  exp_and_rest(g, q.a, m);
+  q.s = f2_all(1.0f);
+  q.r = f2_all(0.0f);
+  if constexpr (SCALE == GDN_SCALE_COMPLEMENT) q.s = m;
   if constexpr (SCALE == GDN_SCALE_SQRT) {
-    const float v = -e * (2.0f + e);  // 1 - a^2
-    q.r = v == 0.0f ? 0.0f : rsqrtf(v);
-    q.s = v * q.r;
+    const F2 var = f2_mul(m, f2_fma(m, f2_all(-1.0f), f2_all(2.0f)));  // 1 - a^2
+    float v0, v1;
+    f2_get(var, v0, v1);
+    // a variance below the smallest normal number counts as zero
+    q.r = f2(rsqrt_hw(fmaxf(v0, 0x1p-126f)), rsqrt_hw(fmaxf(v1, 0x1p-126f)));
+    q.s = f2_mul(var, q.r);
+    if constexpr (BACKWARD) {
+      float r0, r1;
+      f2_get(q.r, r0, r1);
+      q.r = f2(v0 > 0.0f ? r0 : 0.0f, v1 > 0.0f ? r1 : 0.0f);
+    }
   }
   return q;
 }
 
-__device__ __forceinline__ float run_decay(float g_sum) {
-  float a, e;
-  exp_and_m1(g_sum, a, e);
+__device__ __forceinline__ F2 run_decay(F2 g_sum) {
+  F2 a, m;
+  exp_and_rest(g_sum, a, m);
   return a;
 }
 
-// VEC consecutive elements as they lie in memory.
+// VEC channels as they lie in memory; in registers a lane holds two, the second 0 for VEC = 1.
 template <typename T, int VEC>
 struct Raw;
 template <>
 struct Raw<float, 1> {
   float v;
-  __device__ __forceinline__ void get(float* f) const { f[0] = v; }
-  __device__ __forceinline__ void set(const float* f) { v = f[0]; }
+  __device__ __forceinline__ F2 get() const { return f2(v, 0.0f); }
+  __device__ __forceinline__ void set(F2 f) {
+    float rest;
+    f2_get(f, v, rest);
+  }
 };
 template <>
 struct Raw<float, 2> {
   float2 v;
-  __device__ __forceinline__ void get(float* f) const { f[0] = v.x, f[1] = v.y; }
-  __device__ __forceinline__ void set(const float* f) { v = make_float2(f[0], f[1]); }
+  __device__ __forceinline__ F2 get() const { return f2(v.x, v.y); }
+  __device__ __forceinline__ void set(F2 f) { f2_get(f, v.x, v.y); }
 };
 template <>
 struct Raw<__nv_bfloat16, 1> {
   uint16_t v;
-  __device__ __forceinline__ void get(float* f) const { f[0] = __uint_as_float((uint32_t)v << 16); }
-  __device__ __forceinline__ void set(const float* f) { v = __bfloat16_as_ushort(__float2bfloat16_rn(f[0])); }
+  __device__ __forceinline__ F2 get() const { return f2(__uint_as_float((uint32_t)v << 16), 0.0f); }
+  __device__ __forceinline__ void set(F2 f) {
+    float lo, rest;
+    f2_get(f, lo, rest);
+    v = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+  }
 };
 template <>
 struct Raw<__nv_bfloat16, 2> {
   uint32_t v;
-  __device__ __forceinline__ void get(float* f) const { f[0] = bf16_lo(v), f[1] = bf16_hi(v); }
-  __device__ __forceinline__ void set(const float* f) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[0], f[1]);
+  __device__ __forceinline__ F2 get() const { return f2(bf16_lo(v), bf16_hi(v)); }
+  __device__ __forceinline__ void set(F2 f) {
+    float lo, hi;
+    f2_get(f, lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     v = *reinterpret_cast<const uint32_t*>(&h);
   }
 };
 
-// A lane's column of a token array: VEC channels from flat channel c.
+// A lane's column of a token array: VEC channels of every token. Rows are reached by 32-bit
+// offsets from the run's first one (the C entry points bound the stride). The stride passes
+// through an empty asm statement for every run: the compiler otherwise keeps the offsets of all T
+// rows of all arrays in registers through the loop over tiles, and spills.
 template <typename T, int VEC>
 struct Column {
   T* p;
-  int64_t sl;
+  int sl;
   __device__ __forceinline__ Column(const Tok& t, int b, int h, int d)
-      : p(static_cast<T*>(t.p) + channel_offset(t, b, h, d)), sl(t.sl) {}
-  // A cursor on the row of token t. The stride passes through an empty asm statement in every
-  // tile: the compiler otherwise keeps the offsets of all T rows of all arrays in registers
-  // through the loop over tiles, and spills (208 bytes a thread at T = 8, VEC = 2).
-  struct Row {
+      : p(static_cast<T*>(t.p) + channel_offset(t, b, h, d)), sl((int)t.sl) {}
+  struct Run {
     T* p;
-    int64_t sl;
-    __device__ __forceinline__ Raw<T, VEC> load() const {
-      return *reinterpret_cast<const Raw<T, VEC>*>(p);
+    int sl;
+    __device__ __forceinline__ Raw<T, VEC> load(int j) const {
+      return *reinterpret_cast<const Raw<T, VEC>*>(p + j * sl);
     }
-    __device__ __forceinline__ void store(const float* f) const {
+    __device__ __forceinline__ void store(int j, F2 f) const {
       Raw<T, VEC> r;
       r.set(f);
-      *reinterpret_cast<Raw<T, VEC>*>(p) = r;
+      *reinterpret_cast<Raw<T, VEC>*>(p + j * sl) = r;
     }
-    __device__ __forceinline__ void next() { p += sl; }
-    __device__ __forceinline__ void prev() { p -= sl; }
   };
-  __device__ __forceinline__ Row row(int t) const {
-    int64_t s = sl;
-    asm volatile("" : "+l"(s));
-    return Row{p + t * s, s};
+  __device__ __forceinline__ Run run(int t) const {
+    int s = sl;
+    asm volatile("" : "+r"(s));
+    return Run{p + (int64_t)t * s, s};
   }
 };
 
-// Barrier of the W warps of one group.
-template <int W>
-__device__ __forceinline__ void group_sync(int group) {
-  if constexpr (W == kScanWarps)
-    __syncthreads();
-  else if constexpr (W > 1)
-    asm volatile("bar.sync %0, %1;\n" ::"r"(group + 1), "n"(W * 32) : "memory");
+// The tokens of a warp's runs, tile after tile, as the scans read them: gate, input and (backward)
+// the gradient of the output. start() begins with the run at t0, `step` tokens from one tile to
+// the next; take() makes the next run readable; next() may begin the loads after it.
+//
+// RunsInRegisters: any alignment, one tile ahead in registers.
+template <typename Act, int VEC, int T, bool BACKWARD>
+struct RunsInRegisters {
+  static constexpr int kVec = VEC, kTokens = T;
+  static constexpr int kBytes = 0;  // shared memory per warp
+  Column<float, VEC> gate;
+  Column<Act, VEC> in, grad;
+  bool live;
+  int len, t0, step;
+  Raw<float, VEC> next_g[T];
+  Raw<Act, VEC> next_x[T], next_d[BACKWARD ? T : 1], now_x[T], now_d[BACKWARD ? T : 1];
+
+  __device__ __forceinline__ RunsInRegisters(const ScanArgs& a, uint8_t*, int b, int c0, int len_)
+      : gate(a.g, b, 0, 0), in(a.x, b, 0, 0), grad(a.grad_o, b, 0, 0), len(len_) {
+    const int c = c0 + (threadIdx.x & 31) * VEC;
+    live = c < a.C;
+    if (live) {
+      const int h = c / a.D, d = c % a.D;
+      gate = Column<float, VEC>(a.g, b, h, d);
+      in = Column<Act, VEC>(a.x, b, h, d);
+      if constexpr (BACKWARD) grad = Column<Act, VEC>(a.grad_o, b, h, d);
+    }
+  }
+  __device__ __forceinline__ void fetch() {
+    const auto rg = gate.run(t0);
+    const auto rx = in.run(t0), rd = grad.run(t0);
+    const bool whole = live && t0 >= 0 && t0 + T <= len;
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      next_g[j] = {};
+      next_x[j] = {};
+      if constexpr (BACKWARD) next_d[j] = {};
+      if (whole || (live && t0 >= 0 && t0 + j < len)) {
+        next_g[j] = rg.load(j);
+        next_x[j] = rx.load(j);
+        if constexpr (BACKWARD) next_d[j] = rd.load(j);
+      }
+    }
+    t0 += step;
+  }
+  __device__ __forceinline__ void start(int t, int step_) {
+    t0 = t;
+    step = step_;
+    fetch();
+  }
+  __device__ __forceinline__ void take() {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      now_x[j] = next_x[j];
+      if constexpr (BACKWARD) now_d[j] = next_d[j];
+    }
+  }
+  __device__ __forceinline__ void next() { fetch(); }  // once the gates have been read
+  __device__ __forceinline__ F2 g(int j) const { return next_g[j].get(); }
+  __device__ __forceinline__ F2 x(int j) const { return now_x[j].get(); }
+  __device__ __forceinline__ F2 grad_o(int j) const { return now_d[j].get(); }
+};
+
+// RunsInShared: rows that 16-byte pieces cover, copied asynchronously STAGES - 1 tiles ahead into
+// a ring of the warp's own (lane l's channels 2 l and 2 l + 1 of the slab's 64, no bank is asked
+// twice), so that neither the rows in flight nor their addresses take registers.
+template <typename Act, int T, int STAGES, bool BACKWARD>
+struct RunsInShared {
+  static constexpr int kVec = 2, kTokens = T;
+  static constexpr int kWide = 64;  // channels of a slab
+  static constexpr int kAct = T * kWide * (int)sizeof(Act);
+  static constexpr int kStage = T * kWide * 4 + kAct * (BACKWARD ? 2 : 1);
+  static constexpr int kBytes = STAGES * kStage;
+
+  // One lane's pieces of one array: `rows` rows by one instruction of the warp.
+  template <typename E>
+  struct Piece {
+    static constexpr int kElems = 16 / (int)sizeof(E), kPieces = kWide / kElems;
+    static constexpr int kRows = 32 / kPieces;
+    static_assert(T % kRows == 0, "whole instructions per tile");
+    const E* p;
+    int sl;
+    bool live;
+    __device__ __forceinline__ Piece(const Tok& t, const ScanArgs& a, int b, int c0) : sl((int)t.sl) {
+      const int c = c0 + (threadIdx.x & 31) % kPieces * kElems;
+      live = c < a.C;
+      p = static_cast<const E*>(t.p) + channel_offset(t, b, live ? c / a.D : 0, live ? c % a.D : 0);
+    }
+    __device__ __forceinline__ void copy(uint32_t to, int t0, int len) const {
+      const int lane = threadIdx.x & 31;
+#pragma unroll
+      for (int i = 0; i < T; i += kRows) {
+        const int t = t0 + i + lane / kPieces;
+        const bool ok = live && t >= 0 && t < len;
+        const E* from = p + (ok ? (int64_t)t * sl : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                         to + (uint32_t)((i * kPieces + lane) * 16)),
+                     "l"(from), "r"(ok ? 16 : 0)
+                     : "memory");
+      }
+    }
+  };
+
+  Piece<float> gate;
+  Piece<Act> in, grad;
+  int len, t0, step, fill, read;
+  uint32_t ring;
+  const uint8_t* now;
+
+  __device__ __forceinline__ RunsInShared(const ScanArgs& a, uint8_t* shared, int b, int c0, int len_)
+      : gate(a.g, a, b, c0), in(a.x, a, b, c0), grad(BACKWARD ? a.grad_o : a.x, a, b, c0), len(len_),
+        fill(0), read(0), ring(smem_u32(shared)), now(shared) {}
+  __device__ __forceinline__ void fetch() {
+    const uint32_t to = ring + (uint32_t)(fill * kStage);
+    gate.copy(to, t0, len);
+    in.copy(to + T * kWide * 4, t0, len);
+    if constexpr (BACKWARD) grad.copy(to + T * kWide * 4 + kAct, t0, len);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    fill = fill + 1 == STAGES ? 0 : fill + 1;
+    t0 += step;
+  }
+  __device__ __forceinline__ void start(int t, int step_) {
+    t0 = t;
+    step = step_;
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch();
+    now -= kStage;
+    read = -1;
+  }
+  __device__ __forceinline__ void take() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
+    __syncwarp();  // the other lanes' pieces too, and all have read the tile before
+    ++read;
+    now += kStage;
+    if (read == STAGES) {
+      read = 0;
+      now -= kBytes;
+    }
+    fetch();
+  }
+  __device__ __forceinline__ void next() {}
+  __device__ __forceinline__ F2 g(int j) const {
+    return reinterpret_cast<const Raw<float, 2>*>(now)[j * 32 + (threadIdx.x & 31)].get();
+  }
+  __device__ __forceinline__ F2 x(int j) const {
+    return reinterpret_cast<const Raw<Act, 2>*>(now + T * kWide * 4)[j * 32 + (threadIdx.x & 31)].get();
+  }
+  __device__ __forceinline__ F2 grad_o(int j) const {
+    return reinterpret_cast<const Raw<Act, 2>*>(now + T * kWide * 4 + kAct)[j * 32 + (threadIdx.x & 31)].get();
+  }
+};
+
+// Two channels of an fp32 state, the second one only for VEC = 2.
+template <int VEC>
+__device__ __forceinline__ F2 state_load(const float* p) {
+  return f2(p[0], VEC == 2 ? p[VEC - 1] : 0.0f);
 }
+
+template <int VEC>
+__device__ __forceinline__ void state_store(float* p, F2 f) {
+  float lo, hi;
+  f2_get(f, lo, hi);
+  p[0] = lo;
+  if (VEC == 2) p[VEC - 1] = hi;
+}
+
+// One lane's share of what runs hand each other.
+struct Link {
+  F2 a, b;
+};
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
                    : "memory");
 }
 
-// Stores v at the address that p has in the shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ void cluster_store(float* p, int rank, float v) {
+// Stores v at the place that p has in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_store(Link* p, int rank, Link v) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(at), "f"(v) : "memory");
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};\n" ::"r"(at), "l"(v.a.v), "l"(v.b.v)
+               : "memory");
 }
 
-template <typename Act, int SCALE, int VEC, int W, int T, int CL>
-__global__ void __launch_bounds__(kScanWarps * 32, 3) scan_kernel(ScanArgs a, int slabs) {
-  static_assert(CL == 1 || W == kScanWarps, "a cluster's CTAs have one group each");
+constexpr int scan_groups(int W) { return W == 1 ? 8 : 1; }
+constexpr int scan_threads(int W) { return 32 * W * scan_groups(W); }
+
+template <typename Act, int SCALE, class Runs, int W, int CL, int MINB>
+__global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a, int slabs) {
+  constexpr int kGroups = scan_groups(W), VEC = Runs::kVec, T = Runs::kTokens;
+  extern __shared__ __align__(128) uint8_t rings[];
   static_assert(GDN_SCAN_CHUNK % T == 0, "kept states stand where runs begin");
-  constexpr int kGroups = kScanWarps / W;
-  __shared__ float agg[W > 1 ? 2 : 1][kGroups][W > 1 ? W : 1][2 * VEC][W > 1 ? 32 : 1];
-  __shared__ float across[CL > 1 ? 2 : 1][CL][2 * VEC][CL > 1 ? 32 : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int group = warp / W, w = warp % W;
+  __shared__ alignas(16) Link agg[W > 1 ? 2 : 1][W][W > 1 ? 32 : 1];
+  __shared__ alignas(16) Link across[CL > 1 ? 2 : 1][CL][CL > 1 ? 32 : 1];
+  const int lane = threadIdx.x & 31, w = W > 1 ? threadIdx.x >> 5 : 0;
   const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
-  const int64_t unit = CL > 1 ? blockIdx.x / CL : (int64_t)blockIdx.x * kGroups + group;
-  if (unit >= (int64_t)a.B * slabs) return;  // a whole group (CL == 1: no cluster waits for it)
+  const int64_t unit = CL > 1 ? blockIdx.x / CL
+                              : (int64_t)blockIdx.x * kGroups + (W > 1 ? 0 : threadIdx.x >> 5);
+  if (W == 1 && unit >= (int64_t)a.B * slabs) return;  // no barrier waits for this warp
   const int b = (int)(unit / slabs), c = (int)(unit % slabs) * 32 * VEC + lane * VEC;
   const bool live = c < a.C;
   const int hd = live ? c / a.D : 0, d = live ? c % a.D : 0;
   const int len = seq_len(a.lens, b, a.L);
-  const Column<Act, VEC> x(a.x, b, hd, d);
-  const Column<float, VEC> g(a.g, b, hd, d);
   const Column<Act, VEC> o(a.o, b, hd, d);
+  Runs runs(a, rings + (threadIdx.x >> 5) * Runs::kBytes, b, (int)(unit % slabs) * 32 * VEC, len);
   const int64_t state = (int64_t)b * a.C + c;
   float* hist = a.hist && live
                     ? a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + c
                     : nullptr;
-
-  float carry[VEC];  // the state before the tile
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) carry[v] = a.h0 && live ? a.h0[state + v] : 0.0f;
-
-  Raw<float, VEC> next_g[T];
-  Raw<Act, VEC> next_x[T];
-  auto load = [&](int t0) {
-    auto rg = g.row(t0);
-    auto rx = x.row(t0);
-#pragma unroll
-    for (int j = 0; j < T; ++j, rg.next(), rx.next()) {
-      next_g[j] = {};
-      next_x[j] = {};
-      if (live && t0 + j < len) {
-        next_g[j] = rg.load();
-        next_x[j] = rx.load();
-      }
-    }
-  };
+  F2 carry = a.h0 && live ? state_load<VEC>(a.h0 + state) : f2_all(0.0f);  // before the tile
 
   constexpr int kTile = CL * W * T;
   int t0 = (rank * W + w) * T;
-  load(t0);
+  runs.start(t0, kTile);
   if constexpr (CL > 1) cluster_barrier();  // every CTA of the cluster runs before it is written to
   int buf = 0;
   for (int tile = 0; tile < len; tile += kTile, t0 += kTile, buf ^= 1) {
-    float at[T][VEC], u[T][VEC], gsum[VEC], local[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) gsum[v] = local[v] = 0.0f;
+    runs.take();
+    F2 at[T], u[T], g_sum = f2_all(0.0f), local = f2_all(0.0f);
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      float gv[VEC], xv[VEC];
-      next_g[j].get(gv);
-      next_x[j].get(xv);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const Gate q = gate_of<SCALE>(gv[v]);
-        at[j][v] = q.a;
-        u[j][v] = q.s * xv[v];
-        gsum[v] += gv[v];
-        local[v] = fmaf(at[j][v], local[v], u[j][v]);
+      const F2 gj = runs.g(j);
+      const Gate q = gate_of<SCALE>(gj);
+      at[j] = q.a;
+      u[j] = SCALE == GDN_SCALE_NONE ? runs.x(j) : f2_mul(q.s, runs.x(j));
+      if constexpr (W > 1) {
+        g_sum = f2_add(g_sum, gj);
+        local = f2_fma(q.a, local, u[j]);
       }
     }
-    load(t0 + kTile);
-    float h[VEC];  // the state before the warp's run
-    if constexpr (W == 1) {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) h[v] = carry[v];
-    } else {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        agg[buf][group][w][v][lane] = run_decay(gsum[v]);
-        agg[buf][group][w][VEC + v][lane] = local[v];
-      }
-      group_sync<W>(group);
+    runs.next();
+    F2 h = carry;  // the state before the warp's run
+    if constexpr (W > 1) {
+      agg[buf][w][lane] = Link{run_decay(g_sum), local};
+      __syncthreads();
       if constexpr (CL > 1) {
         // the CTA's run, and the part of it before this warp's
-        float pa[VEC], pb[VEC], ca[VEC], cb[VEC];
+        Link before = {f2_all(1.0f), f2_all(0.0f)}, all = before;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          ca[v] = 1.0f;
-          cb[v] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            if (i == w) pa[v] = ca[v], pb[v] = cb[v];
-            const float ai = agg[buf][group][i][v][lane];
-            ca[v] *= ai;
-            cb[v] = fmaf(ai, cb[v], agg[buf][group][i][VEC + v][lane]);
-          }
-          if (w < CL) {
-            cluster_store(&across[buf][rank][v][lane], w, ca[v]);
-            cluster_store(&across[buf][rank][VEC + v][lane], w, cb[v]);
-          }
+        for (int i = 0; i < W; ++i) {
+          if (i == w) before = all;
+          const Link l = agg[buf][i][lane];
+          all.a = f2_mul(l.a, all.a);
+          all.b = f2_fma(l.a, all.b, l.b);
         }
+        for (int r = w; r < CL; r += W) cluster_store(&across[buf][rank][lane], r, all);
         cluster_barrier();
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-          for (int i = 0; i < CL; ++i) {
-            if (i == rank) h[v] = fmaf(pa[v], carry[v], pb[v]);
-            carry[v] = fmaf(across[buf][i][v][lane], carry[v], across[buf][i][VEC + v][lane]);
-          }
+        for (int i = 0; i < CL; ++i) {
+          if (i == rank) h = f2_fma(before.a, carry, before.b);
+          const Link l = across[buf][i][lane];
+          carry = f2_fma(l.a, carry, l.b);
         }
       } else {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            if (i == w) h[v] = carry[v];
-            carry[v] = fmaf(agg[buf][group][i][v][lane], carry[v],
-                            agg[buf][group][i][VEC + v][lane]);
-          }
+        for (int i = 0; i < W; ++i) {
+          if (i == w) h = carry;
+          const Link l = agg[buf][i][lane];
+          carry = f2_fma(l.a, carry, l.b);
         }
       }
     }
-    if (hist && t0 % GDN_SCAN_CHUNK == 0 && t0 < len) {
+    if (hist && t0 % GDN_SCAN_CHUNK == 0 && t0 < len)
+      state_store<VEC>(hist + (int64_t)(t0 / GDN_SCAN_CHUNK) * a.C, h);
+    const auto ro = o.run(t0);
+    if (live && t0 + T <= len) {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) hist[(int64_t)(t0 / GDN_SCAN_CHUNK) * a.C + v] = h[v];
+      for (int j = 0; j < T; ++j) {
+        h = f2_fma(at[j], h, u[j]);
+        ro.store(j, h);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        h = f2_fma(at[j], h, u[j]);
+        if (live && t0 + j < len) ro.store(j, h);
+      }
     }
-    auto ro = o.row(t0);
-#pragma unroll
-    for (int j = 0; j < T; ++j, ro.next()) {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) h[v] = fmaf(at[j][v], h[v], u[j][v]);
-      if (live && t0 + j < len) ro.store(h);
-    }
-    if constexpr (W == 1) {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) carry[v] = h[v];
-    }
+    if constexpr (W == 1) carry = h;
   }
-  if (a.hT && live && rank == 0 && w == 0) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) a.hT[state + v] = carry[v];
-  }
+  if (a.hT && live && rank == 0 && w == 0) state_store<VEC>(a.hT + state, carry);
 }
 
-template <typename Act, int SCALE, int VEC, int W, int T, int CL>
-__global__ void __launch_bounds__(kScanWarps * 32, 2) scan_backward_kernel(ScanArgs a, int slabs) {
-  static_assert(W == kScanWarps && W * T == GDN_SCAN_CHUNK, "a CTA's tile is one kept chunk");
-  __shared__ float agg[2][W][3 * VEC][32];
-  __shared__ float across[CL > 1 ? 2 : 1][CL][2 * VEC][CL > 1 ? 32 : 1];
+// A CTA's tile is one chunk between kept states.
+template <typename Act, int SCALE, class Runs, int CL, int MINB>
+__global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
+    scan_backward_kernel(ScanArgs a, int slabs) {
+  constexpr int T = Runs::kTokens, W = GDN_SCAN_CHUNK / T;
+  constexpr int VEC = Runs::kVec;
+  extern __shared__ __align__(128) uint8_t rings[];
+  __shared__ alignas(16) Link agg[2][W][32];  // decay and forward scan of each run
+  __shared__ F2 agg_back[2][W][32];           // its scan of the gradient
+  __shared__ alignas(16) Link across[CL > 1 ? 2 : 1][CL][CL > 1 ? 32 : 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
   const int64_t unit = blockIdx.x / CL;
@@ -298,167 +446,111 @@ __global__ void __launch_bounds__(kScanWarps * 32, 2) scan_backward_kernel(ScanA
   const bool live = c < a.C;
   const int hd = live ? c / a.D : 0, d = live ? c % a.D : 0;
   const int len = seq_len(a.lens, b, a.L);
-  const Column<Act, VEC> x(a.x, b, hd, d), go(a.grad_o, b, hd, d);
-  const Column<float, VEC> g(a.g, b, hd, d);
   const Column<Act, VEC> gx(a.grad_x, b, hd, d);
   const Column<float, VEC> gg(a.grad_g, b, hd, d);
+  Runs runs(a, rings + w * Runs::kBytes, b, (int)(unit % slabs) * 32 * VEC, len);
   const int64_t state = (int64_t)b * a.C + c;
   const float* hist =
       a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + c;
+  // the gradient that reaches the tile's last state from behind
+  F2 carry = a.h0 && live ? state_load<VEC>(a.h0 + state) : f2_all(0.0f);
 
-  float carry[VEC];  // the gradient that reaches the tile's last state from behind
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) carry[v] = a.h0 && live ? a.h0[state + v] : 0.0f;
-
-  Raw<float, VEC> next_g[T];
-  Raw<Act, VEC> next_x[T], next_o[T];
-  float next_h[VEC];  // the kept state before the CTA's tile
-  auto load = [&](int t0) {
-    auto rg = g.row(t0);
-    auto rx = x.row(t0), rd = go.row(t0);
-#pragma unroll
-    for (int j = 0; j < T; ++j, rg.next(), rx.next(), rd.next()) {
-      next_g[j] = {};
-      next_x[j] = {};
-      next_o[j] = {};
-      if (live && t0 >= 0 && t0 + j < len) {
-        next_g[j] = rg.load();
-        next_x[j] = rx.load();
-        next_o[j] = rd.load();
-      }
-    }
-    const int at = t0 - w * T;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      next_h[v] = live && at >= 0 && at < len ? hist[(int64_t)(at / GDN_SCAN_CHUNK) * a.C + v] : 0.0f;
+  // the kept state before the CTA's tile that begins at `first`
+  auto kept = [&](int first) {
+    return live && first >= 0 && first < len
+               ? state_load<VEC>(hist + (int64_t)(first / GDN_SCAN_CHUNK) * a.C)
+               : f2_all(0.0f);
   };
 
   constexpr int kTile = CL * GDN_SCAN_CHUNK;
-  const int tiles = (int)(((int64_t)len + kTile - 1) / kTile);
+  const int tiles = (len + kTile - 1) / kTile;
   int t0 = (tiles - 1) * kTile + rank * GDN_SCAN_CHUNK + w * T;
-  load(t0);
+  runs.start(t0, -kTile);
+  F2 next_h = kept(t0 - w * T);
   if constexpr (CL > 1) cluster_barrier();  // every CTA of the cluster runs before it is written to
   int buf = 0;
   for (int tile = tiles - 1; tile >= 0; --tile, t0 -= kTile, buf ^= 1) {
-    float at[T][VEC], s[T][VEC], r[T][VEC], gsum[VEC], fwd[VEC], bwd[VEC], h[VEC];
-    Raw<Act, VEC> xr[T], dor[T];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) gsum[v] = fwd[v] = bwd[v] = 0.0f, h[v] = next_h[v];
+    runs.take();
+    F2 at[T], s[T], r[T], g_sum = f2_all(0.0f), fwd = g_sum, bwd = g_sum, h = next_h;
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      float gv[VEC], xv[VEC];
-      xr[j] = next_x[j];
-      dor[j] = next_o[j];
-      next_g[j].get(gv);
-      xr[j].get(xv);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const Gate q = gate_of<SCALE>(gv[v]);
-        at[j][v] = q.a;
-        s[j][v] = q.s;
-        r[j][v] = q.r;
-        gsum[v] += gv[v];
-        fwd[v] = fmaf(q.a, fwd[v], q.s * xv[v]);
-      }
+      const F2 gj = runs.g(j);
+      const Gate q = gate_of<SCALE, true>(gj);
+      at[j] = q.a;
+      s[j] = q.s;
+      r[j] = q.r;
+      g_sum = f2_add(g_sum, gj);
+      fwd = f2_fma(q.a, fwd, f2_mul(q.s, runs.x(j)));
     }
 #pragma unroll
-    for (int j = T - 1; j >= 0; --j) {
-      float dv[VEC];
-      dor[j].get(dv);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) bwd[v] = at[j][v] * (dv[v] + bwd[v]);
-    }
-    load(t0 - kTile);
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      agg[buf][w][v][lane] = run_decay(gsum[v]);
-      agg[buf][w][VEC + v][lane] = fwd[v];
-      agg[buf][w][2 * VEC + v][lane] = bwd[v];
-    }
+    for (int j = T - 1; j >= 0; --j) bwd = f2_mul(at[j], f2_add(runs.grad_o(j), bwd));
+    runs.next();
+    next_h = kept(t0 - w * T - kTile);
+    agg[buf][w][lane] = Link{run_decay(g_sum), fwd};
+    agg_back[buf][w][lane] = bwd;
     __syncthreads();
-    float dc[VEC];  // the gradient that reaches the warp's last state from behind
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < w) h[v] = fmaf(agg[buf][i][v][lane], h[v], agg[buf][i][VEC + v][lane]);
-    }
+    F2 dc = carry;  // the gradient that reaches the warp's last state from behind
     if constexpr (CL > 1) {
-      float pa[VEC], pb[VEC], ca[VEC], cb[VEC];
+      // the CTA's run, and the part of it behind this warp's
+      Link behind = {f2_all(1.0f), f2_all(0.0f)}, all = behind;
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        ca[v] = 1.0f;
-        cb[v] = 0.0f;
+      for (int i = W - 1; i >= 0; --i) {
+        if (i == w) behind = all;
+        const F2 ai = agg[buf][i][lane].a;
+        all.a = f2_mul(ai, all.a);
+        all.b = f2_fma(ai, all.b, agg_back[buf][i][lane]);
+      }
+      for (int r = w; r < CL; r += W) cluster_store(&across[buf][rank][lane], r, all);
 #pragma unroll
-        for (int i = W - 1; i >= 0; --i) {
-          if (i == w) pa[v] = ca[v], pb[v] = cb[v];
-          const float ai = agg[buf][i][v][lane];
-          ca[v] *= ai;
-          cb[v] = fmaf(ai, cb[v], agg[buf][i][2 * VEC + v][lane]);
-        }
-        if (w < CL) {
-          cluster_store(&across[buf][rank][v][lane], w, ca[v]);
-          cluster_store(&across[buf][rank][VEC + v][lane], w, cb[v]);
-        }
+      for (int i = 0; i < W - 1; ++i) {
+        const Link l = agg[buf][i][lane];
+        if (i < w) h = f2_fma(l.a, h, l.b);
       }
       cluster_barrier();
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-        for (int i = CL - 1; i >= 0; --i) {
-          if (i == rank) dc[v] = fmaf(pa[v], carry[v], pb[v]);
-          carry[v] = fmaf(across[buf][i][v][lane], carry[v], across[buf][i][VEC + v][lane]);
-        }
+      for (int i = CL - 1; i >= 0; --i) {
+        if (i == rank) dc = f2_fma(behind.a, carry, behind.b);
+        const Link l = across[buf][i][lane];
+        carry = f2_fma(l.a, carry, l.b);
       }
     } else {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
+      for (int i = 0; i < W - 1; ++i) {
+        const Link l = agg[buf][i][lane];
+        if (i < w) h = f2_fma(l.a, h, l.b);
+      }
 #pragma unroll
-        for (int i = W - 1; i >= 0; --i) {
-          if (i == w) dc[v] = carry[v];
-          carry[v] = fmaf(agg[buf][i][v][lane], carry[v], agg[buf][i][2 * VEC + v][lane]);
-        }
+      for (int i = W - 1; i >= 0; --i) {
+        if (i == w) dc = carry;
+        carry = f2_fma(agg[buf][i][lane].a, carry, agg_back[buf][i][lane]);
       }
     }
-    float before[T][VEC];
+    F2 before[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      float xv[VEC];
-      xr[j].get(xv);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        before[j][v] = h[v];
-        h[v] = fmaf(at[j][v], h[v], s[j][v] * xv[v]);
-      }
+      before[j] = h;
+      h = f2_fma(at[j], h, f2_mul(s[j], runs.x(j)));
     }
-    auto wx = gx.row(t0 + T - 1);
-    auto wg = gg.row(t0 + T - 1);
+    const auto wx = gx.run(t0);
+    const auto wg = gg.run(t0);
+    const bool whole = live && t0 + T <= len;
 #pragma unroll
-    for (int j = T - 1; j >= 0; --j, wx.prev(), wg.prev()) {
-      float xv[VEC], dv[VEC], dx[VEC], dg[VEC];
-      xr[j].get(xv);
-      dor[j].get(dv);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float dh = dv[v] + dc[v];
-        dx[v] = s[j][v] * dh;
-        dc[v] = at[j][v] * dh;
-        // a h dh + s' x dh, with s' = -a for 1 - a and -a^2 / s for sqrt(1 - a^2)
-        float k = before[j][v];
-        if constexpr (SCALE == GDN_SCALE_COMPLEMENT) k -= xv[v];
-        if constexpr (SCALE == GDN_SCALE_SQRT) k = fmaf(-at[j][v] * r[j][v], xv[v], k);
-        dg[v] = dc[v] * k;
-      }
-      if (live && t0 + j < len) {
-        wx.store(dx);
-        wg.store(dg);
+    for (int j = T - 1; j >= 0; --j) {
+      const F2 dh = f2_add(runs.grad_o(j), dc);
+      const F2 dx = f2_mul(s[j], dh);
+      dc = f2_mul(at[j], dh);
+      // a h dh + s' x dh, with s' = -a for 1 - a and -a^2 / s for sqrt(1 - a^2)
+      F2 k = before[j];
+      if constexpr (SCALE == GDN_SCALE_COMPLEMENT) k = f2_fma(runs.x(j), f2_all(-1.0f), k);
+      if constexpr (SCALE == GDN_SCALE_SQRT)
+        k = f2_fma(f2_mul(f2_mul(at[j], f2_all(-1.0f)), r[j]), runs.x(j), k);
+      if (whole || (live && t0 + j < len)) {
+        wx.store(j, dx);
+        wg.store(j, f2_mul(dc, k));
       }
     }
   }
-  if (a.hT && live && rank == 0 && w == 0) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) a.hT[state + v] = carry[v];
-  }
+  if (a.hT && live && rank == 0 && w == 0) state_store<VEC>(a.hT + state, carry);
 }
 
 }  // namespace gdnq

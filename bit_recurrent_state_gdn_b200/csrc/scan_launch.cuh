@@ -5,33 +5,16 @@
 #include <algorithm>
 
 #include "scan_kernels.cuh"
-
+#include "window_dispatch.cuh"
 namespace gdnq {
 
-struct ScanShape {
-  int warps, tokens, cluster;  // template arguments W, T, CL
-};
-
-inline ScanShape scan_shape(int64_t units, int L) {
-  if (L == 1) return {1, 1, 1};
-  if (L <= 8 || units >= 2368) return {1, 8, 1};
-  int cl = 1;
-  while (cl < 8 && units * cl * kScanWarps < 1776 && cl * kScanWarps * 8 < L) cl *= 2;
-  return {kScanWarps, 8, cl};
-}
-
-inline int scan_backward_cluster(int64_t units, int L) {
-  int cl = 1;
-  while (cl < 8 && units * cl * kScanWarps < 1776 && cl * GDN_SCAN_CHUNK < L) cl *= 2;
-  return cl;
-}
-
 template <typename... Params>
-cudaError_t launch_in_clusters(void (*kernel)(Params...), unsigned grid, int cluster,
-                               cudaStream_t st, Params... args) {
+cudaError_t launch_in_clusters(void (*kernel)(Params...), int64_t grid, int threads, int cluster,
+                               int shared, cudaStream_t st, Params... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kScanWarps * 32);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)shared;
   cfg.stream = st;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -42,61 +25,144 @@ cudaError_t launch_in_clusters(void (*kernel)(Params...), unsigned grid, int clu
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename Act, int SCALE, int VEC>
-cudaError_t launch_scan_vec(const ScanArgs& a, bool backward, cudaStream_t st) {
-  const int slabs = (a.C + 32 * VEC - 1) / (32 * VEC);
+template <typename Act, int SCALE, class Runs, int W, int CL, int MINB>
+cudaError_t scan_forward(const ScanArgs& a, int slabs, cudaStream_t st) {
+  constexpr auto kernel = scan_kernel<Act, SCALE, Runs, W, CL, MINB>;
+  constexpr int kThreads = scan_threads(W), kShared = kThreads / 32 * Runs::kBytes;
+  // above 48 KB the limit has to be raised, and the joins' static arrays count too
+  const cudaError_t e = ensure_smem<kernel>(kShared ? std::max(kShared, 48 * 1024 + 16) : 0);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)a.B * slabs;
+  const int64_t grid = (units + scan_groups(W) - 1) / scan_groups(W) * CL;
+  return launch_in_clusters(kernel, grid, kThreads, CL, kShared, st, a, slabs);
+}
+
+template <typename Act, int SCALE, class Runs, int CL, int MINB>
+cudaError_t scan_back(const ScanArgs& a, int slabs, cudaStream_t st) {
+  constexpr auto kernel = scan_backward_kernel<Act, SCALE, Runs, CL, MINB>;
+  constexpr int W = GDN_SCAN_CHUNK / Runs::kTokens, kShared = W * Runs::kBytes;
+  const cudaError_t e = ensure_smem<kernel>(kShared ? std::max(kShared, 48 * 1024 + 16) : 0);
+  if (e != cudaSuccess) return e;
+  return launch_in_clusters(kernel, (int64_t)a.B * slabs * CL, 32 * W, CL, kShared, st, a, slabs);
+}
+
+// CTAs that share a unit (the 32 kVec channels of one sequence) as a cluster: where units are
+// few, as many as two CTAs per SM hold, each with a tile of its own to take.
+inline int scan_cluster(int64_t units, int tile, int L) {
+  int cl = 1;
+  while (cl < 8 && units * cl * 2 <= 296 && cl * tile < L) cl *= 2;
+  return cl;
+}
+
+// How a forward scan shares its units out. Measured on 64 units per sequence, bf16, in GB/s of
+// 6452 (four warps a unit and four CTAs per SM / eight and two):
+//   64 units  2305 / 2833, clusters of four CTAs of eight 4670    128  3973 / 5365
+//   256  5750 / 6074    384  6209 / 5674    512  6415 / 6006    768  5360 / 5953
+//   1024  6149 / 6368   1280  5994 / 6183   1664  6405 / 5938   2560  6337 / 5824
+// so: eight warps where they fit at once or where four leave a second wave half empty. Units of
+// few tokens go to one warp each, eight units a CTA, without joins: 2048 units of 100 tokens 5299
+// against 4248 with four warps, 16384 of 64 tokens 6225 / 4803, 4096 of 512 tokens 6335 / 6571.
+enum class ScanSplit { Alone, Four, Eight };
+
+inline ScanSplit scan_split(int64_t units, int L, int run) {
+  if (L <= run || (units >= 2048 && L <= 256)) return ScanSplit::Alone;
+  return (units > 296 && units <= 592) || units > 1480 ? ScanSplit::Four : ScanSplit::Eight;
+}
+
+template <typename Act, int SCALE, class P>
+cudaError_t launch_scan_plan(const ScanArgs& a, bool backward, cudaStream_t st) {
+  constexpr int kWide = 32 * P::Back::kVec;
+  const int slabs = (a.C + kWide - 1) / kWide;
   const int64_t units = (int64_t)a.B * slabs;
   if (backward) {
-    const int cl = scan_backward_cluster(units, a.L);
-    const unsigned grid = (unsigned)(units * cl);
-    switch (cl) {
+    switch (scan_cluster(units, GDN_SCAN_CHUNK, a.L)) {
       case 1:
-        return launch_in_clusters(scan_backward_kernel<Act, SCALE, VEC, 8, 8, 1>, grid, cl, st, a, slabs);
+        return scan_back<Act, SCALE, typename P::Back, 1, 2>(a, slabs, st);
       case 2:
-        return launch_in_clusters(scan_backward_kernel<Act, SCALE, VEC, 8, 8, 2>, grid, cl, st, a, slabs);
+        return scan_back<Act, SCALE, typename P::Back, 2, 2>(a, slabs, st);
       case 4:
-        return launch_in_clusters(scan_backward_kernel<Act, SCALE, VEC, 8, 8, 4>, grid, cl, st, a, slabs);
+        return scan_back<Act, SCALE, typename P::Back, 4, 2>(a, slabs, st);
       default:
-        return launch_in_clusters(scan_backward_kernel<Act, SCALE, VEC, 8, 8, 8>, grid, cl, st, a, slabs);
+        return scan_back<Act, SCALE, typename P::Back, 8, 2>(a, slabs, st);
     }
   }
-  const ScanShape s = scan_shape(units, a.L);
-  const int groups = kScanWarps / s.warps;
-  const unsigned grid =
-      (unsigned)(s.cluster > 1 ? units * s.cluster : (units + groups - 1) / groups);
-  if (s.tokens == 1)
-    return launch_in_clusters(scan_kernel<Act, SCALE, VEC, 1, 1, 1>, grid, 1, st, a, slabs);
-  if (s.warps == 1)
-    return launch_in_clusters(scan_kernel<Act, SCALE, VEC, 1, 8, 1>, grid, 1, st, a, slabs);
-  switch (s.cluster) {
-    case 1:
-      return launch_in_clusters(scan_kernel<Act, SCALE, VEC, 8, 8, 1>, grid, 1, st, a, slabs);
-    case 2:
-      return launch_in_clusters(scan_kernel<Act, SCALE, VEC, 8, 8, 2>, grid, 2, st, a, slabs);
-    case 4:
-      return launch_in_clusters(scan_kernel<Act, SCALE, VEC, 8, 8, 4>, grid, 4, st, a, slabs);
+  if (a.L <= 1) return scan_forward<Act, SCALE, typename P::One, 1, 1, 4>(a, slabs, st);
+  switch (scan_split(units, a.L, P::Alone::kTokens)) {
+    case ScanSplit::Alone:
+      return scan_forward<Act, SCALE, typename P::Alone, 1, 1, 2>(a, slabs, st);
+    case ScanSplit::Four:
+      return scan_forward<Act, SCALE, typename P::Four, 4, 1, 4>(a, slabs, st);
     default:
-      return launch_in_clusters(scan_kernel<Act, SCALE, VEC, 8, 8, 8>, grid, 8, st, a, slabs);
+      break;
+  }
+  using Eight = typename P::Eight;
+  switch (scan_cluster(units, 8 * Eight::kTokens, a.L)) {
+    case 8:
+      return scan_forward<Act, SCALE, Eight, 8, 8, 2>(a, slabs, st);
+    case 4:
+      return scan_forward<Act, SCALE, Eight, 8, 4, 2>(a, slabs, st);
+    default:  // two CTAs of a cluster gain nothing over one (128 units: 4994 / 5365 GB/s)
+      return scan_forward<Act, SCALE, Eight, 8, 1, 2>(a, slabs, st);
   }
 }
 
-// Pairs of channels may be moved as one when every pair lies in one head and is aligned.
-inline bool pairs(const Tok& t, int D, size_t elem) {
-  return t.p == nullptr ||
-         (D % 2 == 0 && t.sb % 2 == 0 && t.sl % 2 == 0 && t.sh % 2 == 0 &&
-          reinterpret_cast<uintptr_t>(t.p) % (2 * elem) == 0);
+// Rows that 16-byte pieces cover. Runs of 16 tokens against 8 halve the joins (512 units of 4096
+// tokens: 167 / 185 us); two stages of them keep as many bytes in flight as four of 8. Eight warps
+// of fp32 rows would fill an SM's shared memory with one CTA, so theirs are runs of 8.
+template <typename Act>
+struct PlanShared {
+  static constexpr bool kF32 = sizeof(Act) == 4;
+  using One = RunsInRegisters<Act, 2, 1, false>;
+  using Alone = RunsInShared<Act, 8, 4, false>;
+  using Four = RunsInShared<Act, 16, 2, false>;
+  using Eight = RunsInShared<Act, kF32 ? 8 : 16, kF32 ? 3 : 2, false>;
+  using Back = RunsInShared<Act, 16, 2, true>;
+};
+
+// Any other placement: VEC channels at a time.
+template <typename Act, int VEC>
+struct PlanRegisters {
+  using One = RunsInRegisters<Act, VEC, 1, false>;
+  using Alone = RunsInRegisters<Act, VEC, 8, false>;
+  using Four = Alone;
+  using Eight = Alone;
+  using Back = RunsInRegisters<Act, VEC, 8, true>;
+};
+
+// Whether `n` channels may be moved as one in every array: they lie in one head and are aligned.
+inline bool aligned(const Tok& t, int D, int n, size_t elem) {
+  return D % n == 0 && t.sb % n == 0 && t.sl % n == 0 && t.sh % n == 0 &&
+         reinterpret_cast<uintptr_t>(t.p) % (n * elem) == 0;
 }
 
 template <typename Act, int SCALE>
-cudaError_t launch_scan_scale(const ScanArgs& a, bool backward, cudaStream_t st) {
-  bool two = pairs(a.x, a.D, sizeof(Act)) && pairs(a.g, a.D, 4);
-  if (backward)
-    two = two && pairs(a.grad_o, a.D, sizeof(Act)) && pairs(a.grad_x, a.D, sizeof(Act)) &&
-          pairs(a.grad_g, a.D, 4);
-  else
-    two = two && pairs(a.o, a.D, sizeof(Act));
-  return two ? launch_scan_vec<Act, SCALE, 2>(a, backward, st)
-             : launch_scan_vec<Act, SCALE, 1>(a, backward, st);
+cudaError_t launch_scan_scale(ScanArgs a, bool backward, cudaStream_t st) {
+  struct Used {
+    const Tok* t;
+    size_t elem;
+  };
+  const Used read[3] = {{&a.x, sizeof(Act)}, {&a.g, 4}, {backward ? &a.grad_o : &a.x, sizeof(Act)}};
+  const Used written[2] = {{backward ? &a.grad_x : &a.o, sizeof(Act)},
+                           {backward ? &a.grad_g : &a.o, backward ? 4 : sizeof(Act)}};
+  // where a token's heads follow one another in every array, they are one head of C channels
+  bool dense = true;
+  for (const Used& u : read) dense = dense && u.t->sh == a.D;
+  for (const Used& u : written) dense = dense && u.t->sh == a.D;
+  if (dense || a.H == 1) {
+    a.D = a.C;
+    a.H = 1;
+    a.x.sh = a.g.sh = a.o.sh = a.grad_o.sh = a.grad_x.sh = a.grad_g.sh = 0;
+  }
+  bool pairs = true, pieces = true;
+  for (const Used& u : read) {
+    pairs = pairs && aligned(*u.t, a.D, 2, u.elem);
+    pieces = pieces && aligned(*u.t, a.D, (int)(16 / u.elem), u.elem);
+  }
+  for (const Used& u : written) pairs = pairs && aligned(*u.t, a.D, 2, u.elem);
+  // 16-byte pieces, channel pairs, single channels
+  if (pairs && pieces) return launch_scan_plan<Act, SCALE, PlanShared<Act>>(a, backward, st);
+  if (pairs) return launch_scan_plan<Act, SCALE, PlanRegisters<Act, 2>>(a, backward, st);
+  return launch_scan_plan<Act, SCALE, PlanRegisters<Act, 1>>(a, backward, st);
 }
 
 template <typename Act>

@@ -87,6 +87,13 @@ SCAN = [
     (1, 2049, 1, 48, "bf16", "none", "tokens", None),
     (150, 70, 4, 64, "bf16", "sqrt", "tokens", None),
     (37, 190, 16, 128, "f32", "complement", "tokens", None),
+    # every way of sharing the work out: four warps, one warp, clusters of four and two
+    (10, 190, 32, 64, "bf16", "sqrt", "tokens", [190, 0, 1, 64, 65, 128, 129, 189, 16, 17]),
+    (10, 140, 32, 64, "f32", "none", "heads", None),
+    (10, 77, 32, 65, "bf16", "sqrt", "odd", None),
+    (64, 100, 32, 64, "bf16", "complement", "tokens", [100, 3] * 32),
+    (15, 1100, 4, 64, "bf16", "sqrt", "tokens", [1100, 0, 513] * 5),
+    (20, 300, 4, 64, "f32", "sqrt", "wide", [300, 128, 129, 1] * 5),
 ]
 
 
