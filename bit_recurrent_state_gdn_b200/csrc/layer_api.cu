@@ -149,6 +149,12 @@ gdnq::NormArgs norm_args(const gdn_norm_config* c, int32_t L) {
   return a;
 }
 
+cudaError_t launch_norm(const gdnq::NormArgs& a, const gdn_norm_config* c, bool backward,
+                        gdn_stream_t stream) {
+  return c->act_dtype == GDN_DTYPE_F32 ? gdnq::launch_norm_f32(a, backward, (cudaStream_t)stream)
+                                       : gdnq::launch_norm_bf16(a, backward, (cudaStream_t)stream);
+}
+
 // Gradients of parameters that no token reaches.
 gdn_status zero(float* p, size_t n, gdn_stream_t stream, const char* where) {
   if (!p || n == 0) return GDN_OK;
@@ -252,7 +258,7 @@ gdn_status gdn_group_norm(const gdn_norm_config* cfg, int32_t L, const gdn_token
   gdnq::NormArgs a = norm_args(cfg, L);
   a.x = tok(x), a.z = tok(z), a.y = tok(y);
   a.w = w, a.bias = bias, a.lens = lens;
-  const cudaError_t err = gdnq::launch_norm(a, *cfg, (cudaStream_t)stream);
+  const cudaError_t err = launch_norm(a, cfg, false, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_group_norm");
 }
 
@@ -310,7 +316,7 @@ gdn_status gdn_group_norm_backward(const gdn_norm_config* cfg, int32_t L, const 
   a.grad_y = tok(grad_y), a.grad_x = tok(grad_x), a.grad_z = tok(grad_z);
   a.w = w, a.bias = bias, a.grad_w = grad_w, a.grad_bias = grad_bias, a.lens = lens;
   a.partials = static_cast<float*>(workspace);
-  const cudaError_t err = gdnq::launch_norm_backward(a, *cfg, (cudaStream_t)stream);
+  const cudaError_t err = launch_norm(a, cfg, true, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_group_norm_backward");
 }
 

@@ -57,8 +57,8 @@ struct ConvArgs {
 // Forward or backward scan, by activation type; scale is a gdn_input_scale.
 cudaError_t launch_scan_f32(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
 cudaError_t launch_scan_bf16(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
-cudaError_t launch_norm(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st);
-cudaError_t launch_norm_backward(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st);
+cudaError_t launch_norm_f32(const NormArgs& a, bool backward, cudaStream_t st);
+cudaError_t launch_norm_bf16(const NormArgs& a, bool backward, cudaStream_t st);
 size_t norm_backward_workspace(const gdn_norm_config& cfg, int L);
 cudaError_t launch_conv(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st);
 cudaError_t launch_conv_backward(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st);

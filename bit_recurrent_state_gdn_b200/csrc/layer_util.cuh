@@ -26,6 +26,6 @@ __device__ __forceinline__ float rsqrt_hw(float x) {
   return y;
 }
 
-__device__ __forceinline__ float sigmoidf(float u) { return 1.0f / (1.0f + __expf(-u)); }
+__device__ __forceinline__ float sigmoidf(float u) { return __fdividef(1.0f, 1.0f + fast_exp(-u)); }
 
 }  // namespace gdnq

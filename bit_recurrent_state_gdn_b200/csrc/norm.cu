@@ -1,31 +1,29 @@
-// Group norm: launches of the kernels in norm_kernels.cuh.
-#include <algorithm>
-
-#include "norm_kernels.cuh"
+// Group norm: the parameters' gradients from partial sums, and the workspace for them.
+#include "norm_launch.cuh"
 
 namespace gdnq {
+namespace {
 
-__global__ void __launch_bounds__(256) norm_reduce_kernel(NormArgs a, int parts) {
-  __shared__ float2 sum[8][32];
+// grad_w and grad_bias from partials[count][2][D] (per head and channel: [parts][H][2][D]): a CTA
+// takes 32 channels, its 32 warps every 32nd partial sum, added in the same order every time.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(NormArgs a, int64_t count) {
+  __shared__ float2 sum[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = a.per_channel ? (int64_t)a.H * a.D : a.D;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float2 s = make_float2(0.0f, 0.0f);
   if (c < n) {
-    // the partials of channel c: one per part (its head alone), or one per part and head
-    const int d = (int)(c % a.D);
-    const int64_t h0 = c / a.D, step = a.per_channel ? a.H : 1;
-    const int64_t count = a.per_channel ? parts : (int64_t)parts * a.H;
-    for (int64_t i = warp; i < count; i += 8) {
-      const float* p = a.partials + (h0 + i * step) * 2 * a.D + d;
-      s.x += p[0];
-      s.y += p[a.D];
+    const int64_t step = a.per_channel ? a.H : 1;
+    const float* p = a.partials + c / a.D * 2 * a.D + c % a.D;
+    for (int64_t i = warp * step; i < count; i += 32 * step) {
+      s.x += p[i * 2 * a.D];
+      s.y += p[i * 2 * a.D + a.D];
     }
   }
   sum[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < n) {
-    for (int w = 1; w < 8; ++w) {
+    for (int w = 1; w < 32; ++w) {
       s.x += sum[w][lane].x;
       s.y += sum[w][lane].y;
     }
@@ -34,56 +32,27 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(NormArgs a, int parts)
   }
 }
 
-namespace {
+}  // namespace
 
-constexpr int kSms = 148;
-
-int backward_parts(int B, int L, int H) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)B * L, kSms * 8 / std::max(H, 1)));
-}
-
-template <typename Act, int NI>
-cudaError_t go(const NormArgs& a, bool backward, cudaStream_t st) {
-  if (!backward) {
-    const int64_t rows = (int64_t)a.B * a.L * a.H;
-    norm_kernel<Act, NI><<<(unsigned)std::min<int64_t>(rows, kSms * 64), kNormThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  const int parts = backward_parts(a.B, a.L, a.H);
-  norm_backward_kernel<Act, NI><<<(unsigned)parts * (unsigned)a.H, kNormThreads, 0, st>>>(a, parts);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+cudaError_t launch_norm_reduce(const NormArgs& a, int64_t partials, cudaStream_t st) {
   const int64_t n = a.per_channel ? (int64_t)a.H * a.D : a.D;
-  norm_reduce_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(a, parts);
+  norm_reduce_kernel<<<(unsigned)((n + 31) / 32), 1024, 0, st>>>(a, partials);
   return cudaGetLastError();
 }
 
-template <typename Act>
-cudaError_t by_size(const NormArgs& a, bool backward, cudaStream_t st) {
-  if (a.D <= 256) return go<Act, 1>(a, backward, st);
-  if (a.D <= 1024) return go<Act, 4>(a, backward, st);
-  if (a.D <= 4096) return go<Act, 16>(a, backward, st);
-  return go<Act, 32>(a, backward, st);
-}
-
-cudaError_t by_type(const NormArgs& a, const gdn_norm_config& cfg, bool backward,
-                    cudaStream_t st) {
-  return cfg.act_dtype == GDN_DTYPE_F32 ? by_size<float>(a, backward, st)
-                                        : by_size<__nv_bfloat16>(a, backward, st);
-}
-
-}  // namespace
-
-cudaError_t launch_norm(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st) {
-  return by_type(a, cfg, false, st);
-}
-
-cudaError_t launch_norm_backward(const NormArgs& a, const gdn_norm_config& cfg, cudaStream_t st) {
-  return by_type(a, cfg, true, st);
-}
-
+// Large enough for any placement of the arrays, on which the split of the rows depends.
 size_t norm_backward_workspace(const gdn_norm_config& cfg, int L) {
-  return (size_t)backward_parts(cfg.B, L, cfg.H) * (size_t)cfg.H * 2 * (size_t)cfg.D * sizeof(float);
+  const int64_t tokens = (int64_t)cfg.B * L;
+  const bool per_channel = cfg.weight == GDN_WEIGHT_CHANNEL;
+  int64_t most = (int64_t)norm_wide_parts(tokens, cfg.H) * cfg.H;
+  if (cfg.D <= kNormWide) {
+    const int elem = cfg.act_dtype == GDN_DTYPE_F32 ? 4 : 2;
+    most = 0;
+    for (int lanes = 4; lanes <= 32; lanes *= 2)
+      most = std::max(most, norm_partials(norm_plan(cfg.D, cfg.H, tokens, elem, lanes), cfg.H,
+                                          per_channel));
+  }
+  return (size_t)most * 2 * (size_t)cfg.D * sizeof(float);
 }
 
 }  // namespace gdnq

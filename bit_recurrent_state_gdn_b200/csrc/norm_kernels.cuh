@@ -1,6 +1,18 @@
 // Group norm over each head's channels with an activation or a gate, and its gradients
-// (include/gdnq_layer.h). One CTA of 256 threads takes a (token, head) row at a time, NI channels
-// per thread in registers.
+// (include/gdnq_layer.h).
+//
+// Mathematics. A row is one head of one token. Its D channels are read once into registers; the
+// mean and the mean square of what is left of it are two sums over the row's lanes, in that order,
+// so that no difference of large squares is taken. Backward the row is normed again from x (cheaper
+// than reading kept statistics would be to write) and the two row sums of dn and dn n follow.
+//
+// Split. LANES lanes of a warp hold a row, a CTA holds 256 / LANES rows at a time: HB neighbouring
+// heads (a power of two) of TB tokens. A lane keeps its head, so that the weights stay in registers
+// and the sums for their gradients do too, and walks tokens; these sums are joined over the CTA
+// in shared memory, written as partial sums, and added by a second kernel in a fixed order.
+//
+// Bound by HBM: rows come through a ring in shared memory, S rows ahead, each lane copying the
+// pieces that it will read (no barrier in the loop).
 #pragma once
 
 #include "layer_util.cuh"
@@ -8,6 +20,11 @@
 namespace gdnq {
 
 constexpr int kNormThreads = 256;
+
+// How rows are shared out over a launch; made by norm_plan.
+struct NormSplit {
+  int lanes, hb_log, heads_of_blocks, parts;  // blocks of HB heads; CTAs per block of heads
+};
 
 // act(u) and act'(u).
 __device__ __forceinline__ float2 act_slope(int activation, float u) {
@@ -17,14 +34,345 @@ __device__ __forceinline__ float2 act_slope(int activation, float u) {
   return make_float2(u * q, q * fmaf(u, 1.0f - q, 1.0f));
 }
 
+// V elements of Act at p, as floats.
+template <typename Act, int V>
+__device__ __forceinline__ void piece_get(const void* p, float* f) {
+  if constexpr (V == 1) {
+    f[0] = Num<Act>::to_f(*static_cast<const Act*>(p));
+  } else {
+    Num<Act>::template load<V>(static_cast<const Act*>(p), f);
+  }
+}
+
+template <typename Act, int V>
+__device__ __forceinline__ void piece_put(void* p, const float* f) {
+  if constexpr (V == 1) {
+    *static_cast<Act*>(p) = Num<Act>::from_f(f[0]);
+  } else if constexpr (sizeof(Act) == 4) {
+    *static_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+    uint4 w;
+    uint32_t* q = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+      q[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *static_cast<uint4*>(p) = w;
+  }
+}
+
+// A lane's walk over the tokens of its head.
+struct Walk {
+  int b, l, step_b, step_l;
+  int64_t left;  // tokens from here to the end, this one included; <= 0 behind it
+  int64_t step;
+  __device__ __forceinline__ Walk(int64_t first, int64_t step_, int64_t tokens, int L)
+      : b((int)(first / L)), l((int)(first % L)), step_b((int)(step_ / L)), step_l((int)(step_ % L)),
+        left(tokens - first), step(step_) {}
+  __device__ __forceinline__ void next(int L) {
+    b += step_b;
+    l += step_l;
+    if (l >= L) {
+      l -= L;
+      ++b;
+    }
+    left -= step;
+  }
+};
+
+// The pieces of NI x LANES x V channels that one lane reads of each array of a row, N arrays.
+//
+// PiecesInShared: 16-byte pieces, S - 1 rows ahead, in slots of the lane's own.
+template <typename Act, int LANES_, int NI_, int N, int S>
+struct PiecesInShared {
+  static constexpr int LANES = LANES_, NI = NI_, V = 16 / (int)sizeof(Act);
+  static constexpr int kSlot = kNormThreads * 16;
+  static constexpr int kBytes = S * N * NI * kSlot;
+  uint32_t ring;
+  const uint8_t* now;
+  int fill = 0, read = 0;
+  __device__ __forceinline__ PiecesInShared(uint8_t* shared)
+      : ring(smem_u32(shared) + threadIdx.x * 16), now(shared + threadIdx.x * 16) {}
+  // from[n] points at the lane's first piece of array n; ok[i] whether piece i is there
+  __device__ __forceinline__ void fetch(const Act* const (&from)[N], const bool (&ok)[NI]) {
+    const uint32_t to = ring + (uint32_t)(fill * N * NI * kSlot);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (ok[i])
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(
+                           to + (uint32_t)((n * NI + i) * kSlot)),
+                       "l"(from[n] + i * LANES * V)
+                       : "memory");
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    fill = fill + 1 == S ? 0 : fill + 1;
+  }
+  static constexpr int kAhead = S - 1;
+  __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 2) : "memory");
+  }
+  __device__ __forceinline__ void get(int n, int i, float* f) const {
+    piece_get<Act, V>(now + (read * N * NI + n * NI + i) * kSlot, f);
+  }
+  __device__ __forceinline__ void done() { read = read + 1 == S ? 0 : read + 1; }
+};
+
+// PiecesInRegisters: single elements at any alignment, one row ahead.
+template <typename Act, int LANES_, int NI_, int N>
+struct PiecesInRegisters {
+  static constexpr int LANES = LANES_, NI = NI_, V = 1, kBytes = 0, kAhead = 1;
+  Act next[N][NI], now[N][NI];
+  __device__ __forceinline__ PiecesInRegisters(uint8_t*) {}
+  __device__ __forceinline__ void fetch(const Act* const (&from)[N], const bool (&ok)[NI]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (ok[i]) next[n][i] = from[n][i * LANES];
+  }
+  __device__ __forceinline__ void wait() {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) now[n][i] = next[n][i];
+  }
+  __device__ __forceinline__ void get(int n, int i, float* f) const { f[0] = Num<Act>::to_f(now[n][i]); }
+  __device__ __forceinline__ void done() {}
+};
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float s) {
+#pragma unroll
+  for (int m = LANES / 2; m; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
+  return s;
+}
+
+__device__ __forceinline__ int64_t row_offset(const Tok& t, int b, int l, int h) {
+  return b * t.sb + l * t.sl + h * t.sh;
+}
+
+// What the kernels share: the lane's place, and the norm of a row.
+template <class P>
+struct NormLane {
+  static constexpr int LANES = P::LANES, NI = P::NI, V = P::V, E = NI * V;
+  int sub, h, hb, tb, part, first_head;
+  bool head;      // the lane's head exists
+  bool ok[NI];    // its pieces lie within D
+  __device__ __forceinline__ NormLane(const NormArgs& a, const NormSplit& s) {
+    const int group = threadIdx.x / LANES;
+    sub = threadIdx.x % LANES;
+    hb = 1 << s.hb_log;
+    tb = kNormThreads / LANES >> s.hb_log;
+    first_head = (int)(blockIdx.x % (unsigned)s.heads_of_blocks) * hb;
+    part = (int)(blockIdx.x / (unsigned)s.heads_of_blocks);
+    h = first_head + group % hb;
+    head = h < a.H;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) ok[i] = head && (i * LANES + sub) * V < a.D;
+  }
+  __device__ __forceinline__ void weights(const NormArgs& a, const float* w, float fill, float* f) const {
+    const float* p = w + (a.per_channel ? (int64_t)h * a.D : 0);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[i * V + v] = w && ok[i] ? p[(i * LANES + sub) * V + v] : fill;
+  }
+  // x <- n (0 where there is no channel); returns 1 / sqrt(variance + eps)
+  __device__ __forceinline__ float normalise(const NormArgs& a, float* x) const {
+    if (a.center) {
+      float s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s += x[e];
+      const float m = lanes_sum<LANES>(s) * a.inv_d;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = ok[e / V] ? x[e] - m : 0.0f;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(x[e], x[e], s);
+    const float var = fmaf(lanes_sum<LANES>(s), a.inv_d, a.eps);
+    const float rstd = rsqrtf(var);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] *= rstd;
+    return rstd;
+  }
+};
+
+template <typename Act, bool GATE, class P>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a, NormSplit split) {
+  constexpr int N = GATE ? 2 : 1, NI = P::NI, V = P::V, E = NI * V;
+  extern __shared__ __align__(128) uint8_t rings[];
+  const NormLane<P> q(a, split);
+  float w[E], bias[E];
+  q.weights(a, a.w, 0.0f, w);
+  q.weights(a, a.bias, 0.0f, bias);
+  P pieces(rings);
+  const int64_t tokens = (int64_t)a.B * a.L, step = (int64_t)split.parts * q.tb;
+  const int64_t first = (int64_t)q.part * q.tb, mine = threadIdx.x / P::LANES >> split.hb_log;
+  Walk ahead(first + mine, step, tokens, a.L), at = ahead;
+  auto fetch = [&]() {
+    const bool live = ahead.left > 0 && ahead.l < seq_len(a.lens, ahead.b, a.L);
+    bool there[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) there[i] = live && q.ok[i];
+    const Act* from[N];
+    from[0] = static_cast<const Act*>(a.x.p) + row_offset(a.x, ahead.b, ahead.l, q.h) + q.sub * V;
+    if constexpr (GATE)
+      from[1] = static_cast<const Act*>(a.z.p) + row_offset(a.z, ahead.b, ahead.l, q.h) + q.sub * V;
+    pieces.fetch(from, there);
+    ahead.next(a.L);
+  };
+#pragma unroll
+  for (int i = 0; i < P::kAhead; ++i) fetch();
+  for (int64_t t = first; t < tokens; t += step, at.next(a.L)) {
+    pieces.wait();
+    const bool live = at.left > 0 && at.l < seq_len(a.lens, at.b, a.L);
+    float x[E], z[E];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (live && q.ok[i]) {
+        pieces.get(0, i, x + i * V);
+        if constexpr (GATE) pieces.get(1, i, z + i * V);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i * V + v] = z[i * V + v] = 0.0f;
+      }
+    }
+    pieces.done();
+    fetch();
+    q.normalise(a, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float u = fmaf(x[e], w[e], bias[e]);
+      x[e] = GATE ? u * act_slope(a.activation, z[e]).x : act_slope(a.activation, u).x;
+    }
+    Act* y = static_cast<Act*>(a.y.p) + row_offset(a.y, at.b, at.l, q.h) + q.sub * V;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (live && q.ok[i]) piece_put<Act, V>(y + i * P::LANES * V, x + i * V);
+  }
+}
+
+// Shared memory: the ring, then (the loop done) two floats for every channel that a lane holds.
+template <class P>
+constexpr int norm_backward_shared() {
+  constexpr int sums = kNormThreads * P::NI * P::V * 8;
+  return P::kBytes > sums ? P::kBytes : sums;
+}
+
+// Leaves its sums of du n and du at partials[CTA][2][D] (weights shared by the heads) or
+// partials[part][head][2][D].
+template <typename Act, bool GATE, class P>
+__global__ void __launch_bounds__(kNormThreads, P::NI * P::V <= 16 ? 2 : 1) norm_backward_kernel(NormArgs a, NormSplit split) {
+  constexpr int N = GATE ? 3 : 2, NI = P::NI, V = P::V, E = NI * V, LANES = P::LANES;
+  extern __shared__ __align__(128) uint8_t rings[];
+  const NormLane<P> q(a, split);
+  float w[E], bias[E], sw[E], sb[E];
+  q.weights(a, a.w, 0.0f, w);
+  q.weights(a, a.bias, 0.0f, bias);
+#pragma unroll
+  for (int e = 0; e < E; ++e) sw[e] = sb[e] = 0.0f;
+  P pieces(rings);
+  const int64_t tokens = (int64_t)a.B * a.L, step = (int64_t)split.parts * q.tb;
+  const int64_t first = (int64_t)q.part * q.tb, mine = threadIdx.x / LANES >> split.hb_log;
+  Walk ahead(first + mine, step, tokens, a.L), at = ahead;
+  auto fetch = [&]() {
+    const bool live = ahead.left > 0 && ahead.l < seq_len(a.lens, ahead.b, a.L);
+    bool there[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) there[i] = live && q.ok[i];
+    const Act* from[N];
+    from[0] = static_cast<const Act*>(a.x.p) + row_offset(a.x, ahead.b, ahead.l, q.h) + q.sub * V;
+    from[1] = static_cast<const Act*>(a.grad_y.p) + row_offset(a.grad_y, ahead.b, ahead.l, q.h) + q.sub * V;
+    if constexpr (GATE)
+      from[2] = static_cast<const Act*>(a.z.p) + row_offset(a.z, ahead.b, ahead.l, q.h) + q.sub * V;
+    pieces.fetch(from, there);
+    ahead.next(a.L);
+  };
+#pragma unroll
+  for (int i = 0; i < P::kAhead; ++i) fetch();
+  for (int64_t t = first; t < tokens; t += step, at.next(a.L)) {
+    pieces.wait();
+    const bool live = at.left > 0 && at.l < seq_len(a.lens, at.b, a.L);
+    float x[E], dy[E], z[E];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (live && q.ok[i]) {
+        pieces.get(0, i, x + i * V);
+        pieces.get(1, i, dy + i * V);
+        if constexpr (GATE) pieces.get(2, i, z + i * V);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i * V + v] = dy[i * V + v] = z[i * V + v] = 0.0f;
+      }
+    }
+    pieces.done();
+    fetch();
+    const float rstd = q.normalise(a, x);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float u = fmaf(x[e], w[e], bias[e]);
+      const float2 f = act_slope(a.activation, GATE ? z[e] : u);
+      const float du = dy[e] * (GATE ? f.x : f.y);
+      if constexpr (GATE) z[e] = dy[e] * u * f.y;  // grad_z
+      sw[e] = fmaf(du, x[e], sw[e]);
+      sb[e] += du;
+      dy[e] = du * w[e];  // dn
+      s1 += dy[e];
+      s2 = fmaf(dy[e], x[e], s2);
+    }
+    const float m1 = a.center ? lanes_sum<LANES>(s1) * a.inv_d : 0.0f;
+    const float m2 = lanes_sum<LANES>(s2) * a.inv_d;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dy[e] = (dy[e] - fmaf(x[e], m2, m1)) * rstd;
+    Act* gx = static_cast<Act*>(a.grad_x.p) + row_offset(a.grad_x, at.b, at.l, q.h) + q.sub * V;
+    Act* gz = nullptr;
+    if constexpr (GATE)
+      gz = static_cast<Act*>(a.grad_z.p) + row_offset(a.grad_z, at.b, at.l, q.h) + q.sub * V;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (live && q.ok[i]) {
+        piece_put<Act, V>(gx + i * LANES * V, dy + i * V);
+        if constexpr (GATE) piece_put<Act, V>(gz + i * LANES * V, z + i * V);
+      }
+    }
+  }
+  // the CTA's sums, rows in order; the ring is no longer read, but copies may still be landing
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
+  __syncthreads();
+  float2* sums = reinterpret_cast<float2*>(rings);  // [row of the CTA][channel]
+  constexpr int kWide = LANES * E, kRows = kNormThreads / LANES;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    sums[threadIdx.x / LANES * kWide + (e / V * LANES + q.sub) * V + e % V] = make_float2(sw[e], sb[e]);
+  __syncthreads();
+  const int keep = a.per_channel ? q.hb : 1;  // sums that stay apart
+  for (int i = threadIdx.x; i < keep * a.D; i += kNormThreads) {
+    const int j = i / a.D, d = i % a.D;
+    if (a.per_channel && q.first_head + j >= a.H) continue;
+    float2 s = make_float2(0.0f, 0.0f);
+    for (int r = j; r < kRows; r += keep) {
+      const float2 v = sums[r * kWide + d];
+      s.x += v.x;
+      s.y += v.y;
+    }
+    float* p = a.partials +
+               (a.per_channel ? ((int64_t)q.part * a.H + q.first_head + j) : (int64_t)blockIdx.x) * 2 * a.D;
+    p[d] = s.x;
+    p[a.D + d] = s.y;
+  }
+}
+
+// ---- heads of more than 1024 channels: one CTA per row ------------------------------------------
+
 // Sums of (p, q) over the CTA, the same in every thread.
 __device__ __forceinline__ float2 cta_sum(float p, float q) {
   __shared__ float2 part[kNormThreads / 32];
-#pragma unroll
-  for (int m = 16; m; m >>= 1) {
-    p += __shfl_xor_sync(~0u, p, m);
-    q += __shfl_xor_sync(~0u, q, m);
-  }
+  p = lanes_sum<32>(p);
+  q = lanes_sum<32>(q);
   __syncthreads();  // the last call's readers are done
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(p, q);
   __syncthreads();
@@ -55,13 +403,8 @@ __device__ __forceinline__ void row_store(const Tok& t, int64_t at, int D, const
   }
 }
 
-__device__ __forceinline__ int64_t row_offset(const Tok& t, int b, int l, int h) {
-  return b * t.sb + l * t.sl + h * t.sh;
-}
-
-// x <- n, returns 1 / sqrt(variance + eps).
 template <int NI>
-__device__ __forceinline__ float normalise(const NormArgs& a, float* x) {
+__device__ __forceinline__ float normalise_row(const NormArgs& a, float* x) {
   if (a.center) {
     float s = 0.0f;
 #pragma unroll
@@ -74,14 +417,14 @@ __device__ __forceinline__ float normalise(const NormArgs& a, float* x) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) s = fmaf(x[i], x[i], s);
-  const float rstd = 1.0f / sqrtf(cta_sum(s, 0.0f).x * a.inv_d + a.eps);
+  const float rstd = rsqrtf(fmaf(cta_sum(s, 0.0f).x, a.inv_d, a.eps));
 #pragma unroll
   for (int i = 0; i < NI; ++i) x[i] *= rstd;
   return rstd;
 }
 
 template <typename Act, int NI>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(NormArgs a) {
   const int64_t rows = (int64_t)a.B * a.L * a.H;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const int h = (int)(r % a.H), l = (int)(r / a.H % a.L), b = (int)(r / a.H / a.L);
@@ -89,8 +432,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
     float x[NI], z[NI];
     row_load<Act, NI>(a.x, row_offset(a.x, b, l, h), a.D, x);
     if (a.z.p) row_load<Act, NI>(a.z, row_offset(a.z, b, l, h), a.D, z);
-    normalise<NI>(a, x);
-    const int base = a.per_channel ? h * a.D : 0;
+    normalise_row<NI>(a, x);
+    const int64_t base = a.per_channel ? (int64_t)h * a.D : 0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int d = i * kNormThreads + threadIdx.x;
@@ -103,12 +446,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
   }
 }
 
-// CTA = (part, head): it walks every parts-th token of its head and leaves its sums of du n and
-// du in partials[part][head][2][D].
+// CTA = (part, head): every parts-th token of its head.
 template <typename Act, int NI>
-__global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormArgs a, int parts) {
-  const int h = blockIdx.x % a.H, part = blockIdx.x / a.H;
-  const int base = a.per_channel ? h * a.D : 0;
+__global__ void __launch_bounds__(kNormThreads) norm_wide_backward_kernel(NormArgs a, int parts) {
+  const int h = (int)(blockIdx.x % (unsigned)a.H), part = (int)(blockIdx.x / (unsigned)a.H);
+  const int64_t base = a.per_channel ? (int64_t)h * a.D : 0;
   float w[NI], bias[NI], sw[NI], sb[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -124,7 +466,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormArgs a,
     row_load<Act, NI>(a.x, row_offset(a.x, b, l, h), a.D, x);
     row_load<Act, NI>(a.grad_y, row_offset(a.grad_y, b, l, h), a.D, dy);
     if (a.z.p) row_load<Act, NI>(a.z, row_offset(a.z, b, l, h), a.D, z);
-    const float rstd = normalise<NI>(a, x);
+    const float rstd = normalise_row<NI>(a, x);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -141,7 +483,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormArgs a,
     const float2 s = cta_sum(s1, s2);
     const float m1 = a.center ? s.x * a.inv_d : 0.0f, m2 = s.y * a.inv_d;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) dy[i] = (dy[i] - m1 - x[i] * m2) * rstd;
+    for (int i = 0; i < NI; ++i) dy[i] = (dy[i] - fmaf(x[i], m2, m1)) * rstd;
     row_store<Act, NI>(a.grad_x, row_offset(a.grad_x, b, l, h), a.D, dy);
     if (a.z.p) row_store<Act, NI>(a.grad_z, row_offset(a.grad_z, b, l, h), a.D, z);
   }
@@ -155,9 +497,5 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormArgs a,
     }
   }
 }
-
-// grad_w and grad_bias from partials[parts][H][2][D]: 32 channels per CTA, the partial sums
-// shared out over its 8 warps and added in the same order every time.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(NormArgs a, int parts);
 
 }  // namespace gdnq
