@@ -1,68 +1,45 @@
-// Short convolution: launches of the kernels in conv_kernels.cuh.
-#include <algorithm>
-
-#include "conv_kernels.cuh"
+// Short convolution: the parameters' gradients from partial sums, and the workspace for them.
+#include "conv_launch.cuh"
 
 namespace gdnq {
 namespace {
 
-constexpr int kSms = 148;
-
-int conv_runs(int L) { return std::max(1, (int)(((int64_t)L + kConvRun - 1) / kConvRun)); }
-int conv_slabs(int C) { return (C + 31) / 32; }
-int conv_parts(int B, int L, int C) {
-  const int64_t runs = (int64_t)B * conv_runs(L);
-  return (int)std::max<int64_t>(1, std::min<int64_t>((runs + 7) / 8, kSms * 8 / conv_slabs(C)));
-}
-
-template <typename Act, int K>
-cudaError_t go(const ConvArgs& a, bool backward, cudaStream_t st) {
-  const int runs = conv_runs(a.L);
-  if (!backward) {
-    const int64_t n = (int64_t)a.B * runs * a.C;
-    conv_kernel<Act, K><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, runs);
-    return cudaGetLastError();
+// grad_w [C][K] and grad_bias [C] from partials[parts][K + 1][C]: a CTA takes 32 sums, its 32
+// warps every 32nd part, added in the same order every time.
+__global__ void __launch_bounds__(1024) conv_reduce_kernel(ConvArgs a, int parts) {
+  __shared__ float sum[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n = (int64_t)a.C * (a.K + 1), i = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (i < n)
+    for (int p = warp; p < parts; p += 32) s += a.partials[p * n + i];
+  sum[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && i < n) {
+    for (int w = 1; w < 32; ++w) s += sum[w][lane];
+    const int64_t c = i % a.C;
+    const int j = (int)(i / a.C);
+    if (j < a.K)
+      a.grad_w[c * a.K + j] = s;
+    else if (a.grad_bias)
+      a.grad_bias[c] = s;
   }
-  const int slabs = conv_slabs(a.C), parts = conv_parts(a.B, a.L, a.C);
-  conv_backward_kernel<Act, K><<<(unsigned)(slabs * parts), 256, 0, st>>>(a, runs, slabs);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int64_t n = (int64_t)a.C * (K + 1);
-  conv_reduce_kernel<K><<<(unsigned)((n + 127) / 128), 128, 0, st>>>(a, parts);
-  return cudaGetLastError();
-}
-
-template <typename Act>
-cudaError_t by_taps(const ConvArgs& a, bool backward, cudaStream_t st) {
-  switch (a.K) {
-    case 2:
-      return go<Act, 2>(a, backward, st);
-    case 3:
-      return go<Act, 3>(a, backward, st);
-    default:
-      return go<Act, 4>(a, backward, st);
-  }
-}
-
-cudaError_t by_type(const ConvArgs& a, const gdn_conv_config& cfg, bool backward,
-                    cudaStream_t st) {
-  return cfg.act_dtype == GDN_DTYPE_F32 ? by_taps<float>(a, backward, st)
-                                        : by_taps<__nv_bfloat16>(a, backward, st);
 }
 
 }  // namespace
 
-cudaError_t launch_conv(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st) {
-  return by_type(a, cfg, false, st);
+cudaError_t launch_conv_reduce(const ConvArgs& a, int parts, cudaStream_t st) {
+  const int64_t n = (int64_t)a.C * (a.K + 1);
+  conv_reduce_kernel<<<(unsigned)((n + 31) / 32), 1024, 0, st>>>(a, parts);
+  return cudaGetLastError();
 }
 
-cudaError_t launch_conv_backward(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st) {
-  return by_type(a, cfg, true, st);
-}
-
+// Large enough for any placement of the arrays, on which the split depends.
 size_t conv_backward_workspace(const gdn_conv_config& cfg, int L) {
   const int C = cfg.H * cfg.D;
-  return (size_t)conv_parts(cfg.B, L, C) * (size_t)C * (size_t)(cfg.K + 1) * sizeof(float);
+  const int parts = std::max(conv_backward_split(cfg.B, L, C, 4).parts,
+                             conv_backward_split(cfg.B, L, C, 1).parts);
+  return (size_t)parts * (size_t)C * (size_t)(cfg.K + 1) * sizeof(float);
 }
 
 }  // namespace gdnq

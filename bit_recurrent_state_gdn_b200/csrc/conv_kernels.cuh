@@ -1,154 +1,405 @@
-// Causal depthwise convolution over a few tokens, with SiLU, and its gradients
-// (include/gdnq_layer.h). One thread walks a run of tokens of one channel, the last K inputs in
-// registers.
+// Causal depthwise convolution over K tokens, with SiLU, and its gradients
+// (include/gdnq_layer.h).
+//
+// A thread holds V neighbouring channels and walks a run of tokens, the last K inputs (and,
+// backward, the last K gradients dp of the sums p) in registers, so that every array is read and
+// written once but for the K - 1 tokens before (backward, also behind) a run. Backward p is formed
+// again from x, and input s = t - K + 1 has all its gradient, sum_j w_j dp_{t-j}, when token t is
+// done; a run forms the dp of the K - 1 tokens behind it too, without adding them to grad_w.
+//
+// Bound by HBM: rows come K at a time through a ring in shared memory, in slots of the thread's
+// own (no barrier in the loop).
 #pragma once
 
 #include "layer_util.cuh"
 
 namespace gdnq {
 
-constexpr int kConvRun = 32;  // tokens per thread and run
+constexpr int kConvThreads = 256;
 
-// Input of token t of channel c: x, or the state before the first token.
-template <typename Act, int K>
-__device__ __forceinline__ float conv_input(const ConvArgs& a, const Act* x, int b, int c, int t) {
-  if (t >= 0) return Num<Act>::to_f(x[t * a.x.sl]);
-  const Act* s = static_cast<const Act*>(a.state_in);
-  return s ? Num<Act>::to_f(s[((int64_t)b * (K - 1) + t + K - 1) * a.C + c]) : 0.0f;
+// How a launch is shared out: runs per sequence, tokens of a run; backward also the CTAs that
+// take the same channels.
+struct ConvSplit {
+  int runs, run_tokens, columns, parts;
+};
+
+// V elements at p as pairs (V even), or one and a zero.
+template <typename Act, int V>
+struct Vec {
+  static constexpr int P = (V + 1) / 2;
+  static __device__ __forceinline__ void get(const void* p, F2* f) {
+    if constexpr (V == 1) {
+      f[0] = f2(Num<Act>::to_f(*static_cast<const Act*>(p)), 0.0f);
+    } else if constexpr (sizeof(Act) == 4) {
+      const float4 t = *static_cast<const float4*>(p);
+      f[0] = f2(t.x, t.y);
+      f[1] = f2(t.z, t.w);
+    } else {
+      uint32_t t[V / 2];
+      if constexpr (V == 8) *reinterpret_cast<uint4*>(t) = *static_cast<const uint4*>(p);
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(t) = *static_cast<const uint2*>(p);
+#pragma unroll
+      for (int i = 0; i < P; ++i) f[i] = f2(bf16_lo(t[i]), bf16_hi(t[i]));
+    }
+  }
+  static __device__ __forceinline__ void put(void* p, const F2* f) {
+    float lo, hi;
+    if constexpr (V == 1) {
+      f2_get(f[0], lo, hi);
+      *static_cast<Act*>(p) = Num<Act>::from_f(lo);
+    } else if constexpr (sizeof(Act) == 4) {
+      float4 t;
+      f2_get(f[0], t.x, t.y);
+      f2_get(f[1], t.z, t.w);
+      *static_cast<float4*>(p) = t;
+    } else {
+      uint32_t t[V / 2];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        f2_get(f[i], lo, hi);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        t[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if constexpr (V == 8) *static_cast<uint4*>(p) = *reinterpret_cast<uint4*>(t);
+      if constexpr (V == 4) *static_cast<uint2*>(p) = *reinterpret_cast<uint2*>(t);
+    }
+  }
+};
+
+// Rows of N arrays, K at a time from token t on; rows at or behind `end` read as zero.
+//
+// RowsInShared: V elements are 8 or 16 aligned bytes, S - 1 blocks ahead.
+template <typename Act, int V_, int K, int N, int S>
+struct RowsInShared {
+  static constexpr int V = V_, kPiece = V * (int)sizeof(Act), kSlot = kConvThreads * kPiece;
+  static constexpr int kBytes = S * N * K * kSlot;
+  const Act* p[N];
+  int64_t sl[N];
+  uint32_t ring;
+  const uint8_t* now;
+  int t, end, fill, read;
+  __device__ __forceinline__ RowsInShared(uint8_t* shared)
+      : ring(smem_u32(shared) + threadIdx.x * kPiece), now(shared + threadIdx.x * kPiece) {}
+  __device__ __forceinline__ void start(const Act* const (&from)[N], const int64_t (&stride)[N],
+                                        int first, int end_) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) p[n] = from[n], sl[n] = stride[n];
+    t = first;
+    end = end_;
+    fill = 0;
+    read = 0;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    const uint32_t to = ring + (uint32_t)(fill * N * K * kSlot);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const Act* row = p[n] + t * sl[n];
+#pragma unroll
+      for (int j = 0; j < K; ++j, row += sl[n]) {
+        const bool ok = t + j < end;
+        const Act* from = ok ? row : p[n];
+        const uint32_t at = to + (uint32_t)((n * K + j) * kSlot);
+        if constexpr (kPiece == 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(from),
+                       "r"(ok ? 16 : 0)
+                       : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(at), "l"(from),
+                       "r"(ok ? 8 : 0)
+                       : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    t += K;
+    fill = fill + 1 == S ? 0 : fill + 1;
+  }
+  // the next block is there
+  __device__ __forceinline__ void take() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 2) : "memory");
+  }
+  __device__ __forceinline__ void get(int n, int j, F2* f) const {
+    Vec<Act, V>::get(now + (read * N * K + n * K + j) * kSlot, f);
+  }
+  // the block has been read
+  __device__ __forceinline__ void done() {
+    read = read + 1 == S ? 0 : read + 1;
+    fetch();
+  }
+  __device__ __forceinline__ void finish() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+};
+
+// RowsInRegisters: single elements at any alignment, one block ahead.
+template <typename Act, int K, int N>
+struct RowsInRegisters {
+  static constexpr int V = 1, kBytes = 0;
+  const Act* p[N];
+  int64_t sl[N];
+  int t, end;
+  Act next[N][K], now[N][K];
+  __device__ __forceinline__ RowsInRegisters(uint8_t*) {}
+  __device__ __forceinline__ void start(const Act* const (&from)[N], const int64_t (&stride)[N],
+                                        int first, int end_) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) p[n] = from[n], sl[n] = stride[n];
+    t = first;
+    end = end_;
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        next[n][j] = t + j < end ? p[n][(t + j) * sl[n]] : Num<Act>::from_f(0.0f);
+    t += K;
+  }
+  __device__ __forceinline__ void take() {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < K; ++j) now[n][j] = next[n][j];
+    fetch();
+  }
+  __device__ __forceinline__ void get(int n, int j, F2* f) const {
+    f[0] = f2(Num<Act>::to_f(now[n][j]), 0.0f);
+  }
+  __device__ __forceinline__ void done() {}
+  __device__ __forceinline__ void finish() {}
+};
+
+// Input of token t < 0 of channels c ..: what the state holds.
+template <typename Act, int V, int K>
+__device__ __forceinline__ void state_get(const void* state, const ConvArgs& a, int b, int c, int t, F2* f) {
+  if (state == nullptr) {
+#pragma unroll
+    for (int i = 0; i < Vec<Act, V>::P; ++i) f[i] = f2_all(0.0f);
+    return;
+  }
+  Vec<Act, V>::get(static_cast<const Act*>(state) + ((int64_t)b * (K - 1) + t + K - 1) * a.C + c, f);
 }
 
-template <typename Act, int K>
-__global__ void __launch_bounds__(256) conv_kernel(ConvArgs a, int runs) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int c = (int)(i % a.C);
-  const int64_t r = i / a.C;
-  if (r >= (int64_t)a.B * runs) return;
-  const int b = (int)(r / runs), t0 = (int)(r % runs) * kConvRun;
-  const int len = seq_len(a.lens, b, a.L), t1 = min(t0 + kConvRun, len);
-  if (t0 > 0 && t0 >= len) return;
-  const int hd = c / a.D, d = c % a.D;
-  const Act* x = static_cast<const Act*>(a.x.p) + channel_offset(a.x, b, hd, d);
-  Act* y = static_cast<Act*>(a.y.p) + channel_offset(a.y, b, hd, d);
-  float w[K], v[K];
+template <typename Act, int V, int K>
+__device__ __forceinline__ void state_put(void* state, const ConvArgs& a, int b, int c, int t, const F2* f) {
+  Vec<Act, V>::put(static_cast<Act*>(state) + ((int64_t)b * (K - 1) + t + K - 1) * a.C + c, f);
+}
+
+// w[c + v][j] as pairs over v: V K floats in a row.
+template <int V, int K>
+__device__ __forceinline__ void taps(const ConvArgs& a, int c, F2 (&w)[K][(V + 1) / 2],
+                                     F2 (&bias)[(V + 1) / 2]) {
+  float flat[V * K + K] = {};
+  const float* p = a.w + (int64_t)c * K;
+  if (V % 4 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0) {
 #pragma unroll
-  for (int j = 0; j < K; ++j) w[j] = a.w[(int64_t)c * K + j];
-  const float bias = a.bias ? a.bias[c] : 0.0f;
+    for (int i = 0; i < V * K / 4; ++i) {
+      const float4 t = reinterpret_cast<const float4*>(p)[i];
+      flat[4 * i] = t.x, flat[4 * i + 1] = t.y, flat[4 * i + 2] = t.z, flat[4 * i + 3] = t.w;
+    }
+  } else {
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) v[j + 1] = conv_input<Act, K>(a, x, b, c, t0 - K + 1 + j);
-  // the run that begins the sequence also hands the state on: it alone reads state_in, so
-  // state_out may be the same array
-  if (t0 == 0 && a.state_out) {
-    float s[K - 1];
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) s[j] = conv_input<Act, K>(a, x, b, c, len - K + 1 + j);
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-      static_cast<Act*>(a.state_out)[((int64_t)b * (K - 1) + j) * a.C + c] = Num<Act>::from_f(s[j]);
+    for (int i = 0; i < V * K; ++i) flat[i] = p[i];
   }
-  for (int t = t0; t < t1; ++t) {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) v[j] = v[j + 1];
-    v[K - 1] = Num<Act>::to_f(x[t * a.x.sl]);
-    float p = bias;
+  for (int i = 0; i < (V + 1) / 2; ++i) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) p = fmaf(w[j], v[j], p);
-    y[t * a.y.sl] = Num<Act>::from_f(a.activation == GDN_ACT_SILU ? p * sigmoidf(p) : p);
+    for (int j = 0; j < K; ++j) w[j][i] = f2(flat[2 * i * K + j], flat[(2 * i + 1) * K + j]);
+    bias[i] = f2_all(0.0f);
+    if (a.bias) bias[i] = f2(a.bias[c + 2 * i], V > 1 ? a.bias[c + 2 * i + (V > 1)] : 0.0f);
   }
 }
 
-// CTA = 32 channels x 8 runs at a time; its sums of dp x and dp go to partials[part][C][K + 1].
-template <typename Act, int K>
-__global__ void __launch_bounds__(256) conv_backward_kernel(ConvArgs a, int runs, int slabs) {
-  __shared__ float sum[8][32][K + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int slab = blockIdx.x % slabs, part = blockIdx.x / slabs, parts = gridDim.x / slabs;
-  const int c = slab * 32 + lane;
-  float w[K], dw[K], db = 0.0f, bias = 0.0f;
+template <typename Act, int K, bool SILU, class Rows, int MINB>
+__global__ void __launch_bounds__(kConvThreads, MINB) conv_kernel(ConvArgs a, ConvSplit split) {
+  constexpr int V = Rows::V, P = Vec<Act, V>::P;
+  extern __shared__ __align__(128) uint8_t rings[];
+  // a thread keeps its channels, whose taps it reads once, and takes every split.parts-th run
+  const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+  if (i >= (int64_t)split.parts * split.columns) return;
+  const int c = (int)(i % split.columns) * V, hd = c / a.D, d = c % a.D;
+  F2 w[K][P], bias[P];
+  taps<V, K>(a, c, w, bias);
+  Rows rows(rings);
+  for (int64_t r = i / split.columns; r < (int64_t)a.B * split.runs; r += split.parts) {
+    const int b = (int)(r / split.runs), t0 = (int)(r % split.runs) * split.run_tokens;
+    const int len = seq_len(a.lens, b, a.L), t1 = min(t0 + split.run_tokens, len);
+    if (t0 > 0 && t0 >= len) continue;
+    const Act* x = static_cast<const Act*>(a.x.p) + channel_offset(a.x, b, hd, d);
+    Act* y = static_cast<Act*>(a.y.p) + channel_offset(a.y, b, hd, d) + t0 * a.y.sl;
+    const Act* const from[1] = {x};
+    const int64_t stride[1] = {a.x.sl};
+    if (t0 < t1) rows.start(from, stride, t0, t1);
+    F2 win[K][P];  // win[i]: the input of the last token t with (t - t0) % K == i
 #pragma unroll
-  for (int j = 0; j < K; ++j) dw[j] = 0.0f;
-  if (c < a.C) {
+    for (int j = 0; j < K - 1; ++j) {
+      const int t = t0 - (K - 1) + j;
+      if (t >= 0)
+        Vec<Act, V>::get(x + t * a.x.sl, win[j + 1]);
+      else
+        state_get<Act, V, K>(a.state_in, a, b, c, t, win[j + 1]);
+    }
+    // What the sequence leaves. In one run of K - 1 tokens or more the window has it in the end.
+    // Else the run that begins the sequence hands it on: it alone reads state_in, which state_out
+    // may be.
+    const bool from_window = split.runs == 1 && len >= K - 1;
+    if (a.state_out && t0 == 0 && !from_window) {
+      F2 keep[K - 1][P];
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        const int t = len - (K - 1) + j;
+        if (t >= 0)
+          Vec<Act, V>::get(x + t * a.x.sl, keep[j]);
+        else
+          state_get<Act, V, K>(a.state_in, a, b, c, t, keep[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) state_put<Act, V, K>(a.state_out, a, b, c, j - (K - 1), keep[j]);
+    }
+    for (int t = t0; t < t1; t += K) {
+      rows.take();
+#pragma unroll
+      for (int u = 0; u < K; ++u) {
+        rows.get(0, u, win[u]);
+        F2 out[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          F2 p = bias[e];
+#pragma unroll
+          for (int j = 0; j < K; ++j) p = f2_fma(w[j][e], win[(u + 1 + j) % K][e], p);
+          F2 slope;
+          act_pair<SILU ? GDN_ACT_SILU : GDN_ACT_NONE, false>(p, out[e], slope);
+        }
+        if (t + u < t1) {
+          Vec<Act, V>::put(y, out);
+          y += a.y.sl;
+          if (a.state_out && from_window && t + u >= len - (K - 1))
+            state_put<Act, V, K>(a.state_out, a, b, c, t + u - len, win[u]);
+        }
+      }
+      rows.done();
+    }
+    rows.finish();
+  }
+}
+
+// CTA = TX columns x TY runs at a time; its sums of dp x and dp go to partials[part][K + 1][C].
+template <typename Act, int K, bool SILU, class Rows, int TX, int MINB>
+__global__ void __launch_bounds__(kConvThreads, MINB) conv_backward_kernel(ConvArgs a, ConvSplit split) {
+  constexpr int V = Rows::V, P = Vec<Act, V>::P, TY = kConvThreads / TX;
+  extern __shared__ __align__(128) uint8_t rings[];
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int slabs = (split.columns + TX - 1) / TX;
+  const int slab = (int)(blockIdx.x % (unsigned)slabs), part = (int)(blockIdx.x / (unsigned)slabs);
+  const int column = slab * TX + tx, c = column * V;
+  F2 w[K][P], bias[P], dw[K][P], db[P];
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    db[e] = f2_all(0.0f);
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j][e] = f2_all(0.0f);
+  }
+  Rows rows(rings);
+  if (column < split.columns) {
     const int hd = c / a.D, d = c % a.D;
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[j] = a.w[(int64_t)c * K + j];
-    if (a.bias) bias = a.bias[c];
-    const Act* gso = static_cast<const Act*>(a.grad_state_out);
-    Act* gsi = static_cast<Act*>(a.grad_state_in);
-    for (int64_t r = (int64_t)part * 8 + warp; r < (int64_t)a.B * runs; r += (int64_t)parts * 8) {
-      const int b = (int)(r / runs), t0 = (int)(r % runs) * kConvRun;
-      const int len = seq_len(a.lens, b, a.L), t1 = min(t0 + kConvRun, len);
+    taps<V, K>(a, c, w, bias);
+    for (int64_t r = (int64_t)part * TY + ty; r < (int64_t)a.B * split.runs;
+         r += (int64_t)split.parts * TY) {
+      const int b = (int)(r / split.runs), t0 = (int)(r % split.runs) * split.run_tokens;
+      const int len = seq_len(a.lens, b, a.L), t1 = min(t0 + split.run_tokens, len);
       if (t0 > 0 && t0 >= len) continue;
       const Act* x = static_cast<const Act*>(a.x.p) + channel_offset(a.x, b, hd, d);
       const Act* gy = static_cast<const Act*>(a.grad_y.p) + channel_offset(a.grad_y, b, hd, d);
-      Act* gx = static_cast<Act*>(a.grad_x.p) + channel_offset(a.grad_x, b, hd, d);
-      float v[K], dp[K];  // inputs t-K+1 .. t; dp[j] of token t - j
+      Act* gx = static_cast<Act*>(a.grad_x.p) + channel_offset(a.grad_x, b, hd, d) +
+                (t0 - (K - 1)) * a.grad_x.sl;  // input s = t - K + 1, from t = t0 on
+      const Act* const from[2] = {x, gy};
+      const int64_t stride[2] = {a.x.sl, a.grad_y.sl};
+      rows.start(from, stride, t0, min(t1 + K - 1, len));
+      F2 win[K][P], dp[K][P];  // of the last token t with (t - t0) % K == i
 #pragma unroll
-      for (int j = 0; j < K; ++j) dp[j] = 0.0f;
+      for (int j = 0; j < K - 1; ++j) {
+        const int t = t0 - (K - 1) + j;
+        if (t >= 0)
+          Vec<Act, V>::get(x + t * a.x.sl, win[j + 1]);
+        else
+          state_get<Act, V, K>(a.state_in, a, b, c, t, win[j + 1]);
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) v[j + 1] = conv_input<Act, K>(a, x, b, c, t0 - K + 1 + j);
-      for (int t = t0; t < t1 + K - 1; ++t) {
-#pragma unroll
-        for (int j = K - 1; j > 0; --j) dp[j] = dp[j - 1];
-        dp[0] = 0.0f;
-        if (t < len) {
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) v[j] = v[j + 1];
-          v[K - 1] = Num<Act>::to_f(x[t * a.x.sl]);
-          float p = bias;
-#pragma unroll
-          for (int j = 0; j < K; ++j) p = fmaf(w[j], v[j], p);
-          dp[0] = Num<Act>::to_f(gy[t * a.grad_y.sl]);
-          if (a.activation == GDN_ACT_SILU) {
-            const float q = sigmoidf(p);
-            dp[0] *= q * fmaf(p, 1.0f - q, 1.0f);
-          }
-          if (t < t1) {
-            db += dp[0];
-#pragma unroll
-            for (int j = 0; j < K; ++j) dw[j] = fmaf(dp[0], v[j], dw[j]);
-          }
-        }
-        // the gradient of input s = t - K + 1 is complete
-        const int s = t - (K - 1), u = t - len;
-        if (s < t0 && t0 > 0) continue;
-        float g = 0.0f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) g = fmaf(w[j], dp[j], g);
-        if (gso && u >= 0) g += Num<Act>::to_f(gso[((int64_t)b * (K - 1) + u) * a.C + c]);
-        if (s >= 0)
-          gx[s * a.grad_x.sl] = Num<Act>::from_f(g);
-        else if (gsi)
-          gsi[((int64_t)b * (K - 1) + t) * a.C + c] = Num<Act>::from_f(g);
+        for (int e = 0; e < P; ++e) dp[j + 1][e] = f2_all(0.0f);
       }
+      for (int t = t0; t < t1 + K - 1; t += K) {
+        rows.take();
+#pragma unroll
+        for (int u = 0; u < K; ++u) {
+          F2 dy[P], g[P];
+          rows.get(0, u, win[u]);
+          rows.get(1, u, dy);
+          const float mine = t + u < t1 ? 1.0f : 0.0f;  // dp behind the run is another run's
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            F2 p = bias[e];
+#pragma unroll
+            for (int j = 0; j < K; ++j) p = f2_fma(w[j][e], win[(u + 1 + j) % K][e], p);
+            F2 v, slope;
+            act_pair<SILU ? GDN_ACT_SILU : GDN_ACT_NONE, true>(p, v, slope);
+            dp[u][e] = f2_mul(dy[e], slope);
+            const F2 own = f2_mul(dp[u][e], f2_all(mine));
+            db[e] = f2_add(db[e], own);
+#pragma unroll
+            for (int j = 0; j < K; ++j) dw[j][e] = f2_fma(own, win[(u + 1 + j) % K][e], dw[j][e]);
+            // token t + u - j has dp[(u - j) mod K]
+            g[e] = f2_mul(w[0][e], dp[u][e]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) g[e] = f2_fma(w[j][e], dp[(u + K - j) % K][e], g[e]);
+          }
+          const int s = t + u - (K - 1), behind = t + u - len;
+          if (t + u < t1 + K - 1 && (s >= t0 || t0 == 0)) {
+            if (behind >= 0 && a.grad_state_out) {
+              F2 more[P];
+              state_get<Act, V, K>(a.grad_state_out, a, b, c, behind - (K - 1), more);
+#pragma unroll
+              for (int e = 0; e < P; ++e) g[e] = f2_add(g[e], more[e]);
+            }
+            if (s >= 0)
+              Vec<Act, V>::put(gx, g);
+            else if (a.grad_state_in)
+              state_put<Act, V, K>(a.grad_state_in, a, b, c, s, g);
+          }
+          gx += a.grad_x.sl;
+        }
+        rows.done();
+      }
+      rows.finish();
     }
   }
-#pragma unroll
-  for (int j = 0; j < K; ++j) sum[warp][lane][j] = dw[j];
-  sum[warp][lane][K] = db;
+  // the CTA's sums over its runs, in order
   __syncthreads();
-  if (warp == 0 && c < a.C) {
-    float* p = a.partials + ((int64_t)part * a.C + c) * (K + 1);
+  float* sums = reinterpret_cast<float*>(rings);  // [TY][K + 1][TX V]
+  constexpr int kWide = TX * V;
 #pragma unroll
-    for (int j = 0; j <= K; ++j) {
-      float s = 0.0f;
-      for (int q = 0; q < 8; ++q) s += sum[q][lane][j];
-      p[j] = s;
+  for (int j = 0; j <= K; ++j) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      float lo, hi;
+      f2_get(j < K ? dw[j < K ? j : 0][e] : db[e], lo, hi);
+      float* at = sums + (ty * (K + 1) + j) * kWide + tx * V + 2 * e;
+      at[0] = lo;
+      if constexpr (V > 1) at[1] = hi;
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (K + 1) * kWide; i += kConvThreads) {
+    const int64_t channel = (int64_t)slab * kWide + i % kWide;
+    if (channel >= a.C) continue;
+    float s = 0.0f;
+    for (int q = 0; q < TY; ++q) s += sums[q * (K + 1) * kWide + i];
+    a.partials[((int64_t)part * (K + 1) + i / kWide) * a.C + channel] = s;
   }
 }
 
-// grad_w and grad_bias: the sum over the parts, in order.
-template <int K>
-__global__ void __launch_bounds__(128) conv_reduce_kernel(ConvArgs a, int parts) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, n = (int64_t)a.C * (K + 1);
-  if (i >= n) return;
-  float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s += a.partials[p * n + i];
-  const int64_t c = i / (K + 1);
-  const int j = (int)(i % (K + 1));
-  if (j < K)
-    a.grad_w[c * K + j] = s;
-  else if (a.grad_bias)
-    a.grad_bias[c] = s;
+template <int K, int TX, class Rows>
+constexpr int conv_backward_shared() {
+  constexpr int sums = kConvThreads * (K + 1) * Rows::V * 4;
+  return Rows::kBytes > sums ? Rows::kBytes : sums;
 }
 
 }  // namespace gdnq

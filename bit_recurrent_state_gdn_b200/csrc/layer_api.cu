@@ -155,6 +155,12 @@ cudaError_t launch_norm(const gdnq::NormArgs& a, const gdn_norm_config* c, bool 
                                        : gdnq::launch_norm_bf16(a, backward, (cudaStream_t)stream);
 }
 
+cudaError_t launch_conv(const gdnq::ConvArgs& a, const gdn_conv_config* c, bool backward,
+                        gdn_stream_t stream) {
+  return c->act_dtype == GDN_DTYPE_F32 ? gdnq::launch_conv_f32(a, backward, (cudaStream_t)stream)
+                                       : gdnq::launch_conv_bf16(a, backward, (cudaStream_t)stream);
+}
+
 // Gradients of parameters that no token reaches.
 gdn_status zero(float* p, size_t n, gdn_stream_t stream, const char* where) {
   if (!p || n == 0) return GDN_OK;
@@ -342,7 +348,7 @@ gdn_status gdn_short_conv(const gdn_conv_config* cfg, int32_t L, const gdn_token
   a.w = w, a.bias = bias, a.state_in = state_in, a.state_out = state_out, a.lens = lens;
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D, a.K = cfg->K;
   a.activation = cfg->activation;
-  const cudaError_t err = gdnq::launch_conv(a, *cfg, (cudaStream_t)stream);
+  const cudaError_t err = launch_conv(a, cfg, false, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_short_conv");
 }
 
@@ -397,7 +403,7 @@ gdn_status gdn_short_conv_backward(const gdn_conv_config* cfg, int32_t L, const 
   a.partials = static_cast<float*>(workspace);
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D, a.K = cfg->K;
   a.activation = cfg->activation;
-  const cudaError_t err = gdnq::launch_conv_backward(a, *cfg, (cudaStream_t)stream);
+  const cudaError_t err = launch_conv(a, cfg, true, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_short_conv_backward");
 }
 

@@ -60,8 +60,8 @@ cudaError_t launch_scan_bf16(const ScanArgs& a, int scale, bool backward, cudaSt
 cudaError_t launch_norm_f32(const NormArgs& a, bool backward, cudaStream_t st);
 cudaError_t launch_norm_bf16(const NormArgs& a, bool backward, cudaStream_t st);
 size_t norm_backward_workspace(const gdn_norm_config& cfg, int L);
-cudaError_t launch_conv(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st);
-cudaError_t launch_conv_backward(const ConvArgs& a, const gdn_conv_config& cfg, cudaStream_t st);
+cudaError_t launch_conv_f32(const ConvArgs& a, bool backward, cudaStream_t st);
+cudaError_t launch_conv_bf16(const ConvArgs& a, bool backward, cudaStream_t st);
 size_t conv_backward_workspace(const gdn_conv_config& cfg, int L);
 
 }  // namespace gdnq

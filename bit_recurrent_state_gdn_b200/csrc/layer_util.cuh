@@ -28,4 +28,31 @@ __device__ __forceinline__ float rsqrt_hw(float x) {
 
 __device__ __forceinline__ float sigmoidf(float u) { return __fdividef(1.0f, 1.0f + fast_exp(-u)); }
 
+__device__ __forceinline__ F2 f2_all(float x) { return f2(x, x); }
+
+__device__ __forceinline__ float rcp_hw(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// act(u), and act'(u) where it is asked for.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ void act_pair(F2 u, F2& v, F2& slope) {
+  if constexpr (ACT == GDN_ACT_NONE) {
+    v = u;
+    slope = f2_all(1.0f);
+  } else {
+    float y0, y1, d0, d1;
+    f2_get(f2_mul(u, f2_all(-1.4426950408889634f)), y0, y1);
+    f2_get(f2_add(f2(exp2_hw(y0), exp2_hw(y1)), f2_all(1.0f)), d0, d1);
+    const F2 q = f2(rcp_hw(d0), rcp_hw(d1));  // the sigmoid
+    v = ACT == GDN_ACT_SILU ? f2_mul(u, q) : q;
+    if constexpr (SLOPE) {
+      const F2 rest = f2_fma(q, f2_all(-1.0f), f2_all(1.0f));
+      slope = ACT == GDN_ACT_SILU ? f2_fma(v, rest, q) : f2_mul(q, rest);
+    }
+  }
+}
+
 }  // namespace gdnq

@@ -49,7 +49,7 @@ size_t norm_backward_workspace(const gdn_norm_config& cfg, int L) {
     const int elem = cfg.act_dtype == GDN_DTYPE_F32 ? 4 : 2;
     most = 0;
     for (int lanes = 4; lanes <= 32; lanes *= 2)
-      most = std::max(most, norm_partials(norm_plan(cfg.D, cfg.H, tokens, elem, lanes), cfg.H,
+      most = std::max(most, norm_partials(norm_plan(cfg.D, cfg.H, tokens, elem, lanes, 3), cfg.H,
                                           per_channel));
   }
   return (size_t)most * 2 * (size_t)cfg.D * sizeof(float);

@@ -15,6 +15,8 @@
 // pieces that it will read (no barrier in the loop).
 #pragma once
 
+#include <type_traits>
+
 #include "layer_util.cuh"
 
 namespace gdnq {
@@ -37,11 +39,10 @@ __device__ __forceinline__ float2 act_slope(int activation, float u) {
 // V elements of Act at p, as floats.
 template <typename Act, int V>
 __device__ __forceinline__ void piece_get(const void* p, float* f) {
-  if constexpr (V == 1) {
+  if constexpr (V == 1)
     f[0] = Num<Act>::to_f(*static_cast<const Act*>(p));
-  } else {
+  else
     Num<Act>::template load<V>(static_cast<const Act*>(p), f);
-  }
 }
 
 template <typename Act, int V>
@@ -62,22 +63,40 @@ __device__ __forceinline__ void piece_put(void* p, const float* f) {
   }
 }
 
-// A lane's walk over the tokens of its head.
+// A lane's walk over the tokens of its head, every step-th one; an Offset follows it through one
+// array without multiplications.
 struct Walk {
   int b, l, step_b, step_l;
-  int64_t left;  // tokens from here to the end, this one included; <= 0 behind it
-  int64_t step;
+  int64_t left, step;  // tokens from here to the end, this one included; <= 0 behind it
+  bool wrapped;        // by the last next()
   __device__ __forceinline__ Walk(int64_t first, int64_t step_, int64_t tokens, int L)
       : b((int)(first / L)), l((int)(first % L)), step_b((int)(step_ / L)), step_l((int)(step_ % L)),
-        left(tokens - first), step(step_) {}
+        left(tokens - first), step(step_), wrapped(false) {}
   __device__ __forceinline__ void next(int L) {
     b += step_b;
     l += step_l;
-    if (l >= L) {
+    wrapped = l >= L;
+    if (wrapped) {
       l -= L;
       ++b;
     }
     left -= step;
+  }
+  __device__ __forceinline__ bool live(const int32_t* lens, int L) const {
+    return left > 0 && (lens == nullptr || l < seq_len(lens, b, L));
+  }
+};
+
+template <typename Act>
+struct Offset {
+  Act* p;
+  int64_t step, wrap;
+  __device__ __forceinline__ Offset(const Tok& t, const Walk& w, int h, int d, int L)
+      : p(static_cast<Act*>(t.p) + (w.b * t.sb + w.l * t.sl + h * t.sh + d)),
+        step(w.step_b * t.sb + w.step_l * t.sl), wrap(t.sb - L * t.sl) {}
+  __device__ __forceinline__ void next(const Walk& w) {
+    p += step;
+    if (w.wrapped) p += wrap;
   }
 };
 
@@ -94,18 +113,19 @@ struct PiecesInShared {
   int fill = 0, read = 0;
   __device__ __forceinline__ PiecesInShared(uint8_t* shared)
       : ring(smem_u32(shared) + threadIdx.x * 16), now(shared + threadIdx.x * 16) {}
-  // from[n] points at the lane's first piece of array n; ok[i] whether piece i is there
-  __device__ __forceinline__ void fetch(const Act* const (&from)[N], const bool (&ok)[NI]) {
+  // from[n] points at the lane's first piece of array n, ok[i] says whether piece i is there: a
+  // copy of no bytes fills its slot with zeros, so that the row is read without conditions
+  __device__ __forceinline__ void fetch(const Act* const (&from)[N], const Act* const (&base)[N],
+                                        const bool (&ok)[NI]) {
     const uint32_t to = ring + (uint32_t)(fill * N * NI * kSlot);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (ok[i])
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(
-                           to + (uint32_t)((n * NI + i) * kSlot)),
-                       "l"(from[n] + i * LANES * V)
-                       : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                         to + (uint32_t)((n * NI + i) * kSlot)),
+                     "l"(ok[i] ? from[n] + i * LANES * V : base[n]), "r"(ok[i] ? 16 : 0)
+                     : "memory");
     asm volatile("cp.async.commit_group;\n" ::: "memory");
     fill = fill + 1 == S ? 0 : fill + 1;
   }
@@ -125,12 +145,13 @@ struct PiecesInRegisters {
   static constexpr int LANES = LANES_, NI = NI_, V = 1, kBytes = 0, kAhead = 1;
   Act next[N][NI], now[N][NI];
   __device__ __forceinline__ PiecesInRegisters(uint8_t*) {}
-  __device__ __forceinline__ void fetch(const Act* const (&from)[N], const bool (&ok)[NI]) {
+  __device__ __forceinline__ void fetch(const Act* const (&from)[N], const Act* const (&)[N],
+                                        const bool (&ok)[NI]) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (ok[i]) next[n][i] = from[n][i * LANES];
+        next[n][i] = ok[i] ? from[n][i * LANES] : Num<Act>::from_f(0.0f);
   }
   __device__ __forceinline__ void wait() {
 #pragma unroll
@@ -153,13 +174,20 @@ __device__ __forceinline__ int64_t row_offset(const Tok& t, int b, int l, int h)
   return b * t.sb + l * t.sl + h * t.sh;
 }
 
+__device__ __forceinline__ float f2_sum(F2 a) {
+  float lo, hi;
+  f2_get(a, lo, hi);
+  return lo + hi;
+}
+
 // What the kernels share: the lane's place, and the norm of a row.
 template <class P>
 struct NormLane {
-  static constexpr int LANES = P::LANES, NI = P::NI, V = P::V, E = NI * V;
+  // a lane's channels two by two (the second of an only one is 0): channel c = i V + v is half
+  // c % 2 of pair c / 2
+  static constexpr int LANES = P::LANES, NI = P::NI, V = P::V, E = (NI * V + 1) / 2;
   int sub, h, hb, tb, part, first_head;
-  bool head;      // the lane's head exists
-  bool ok[NI];    // its pieces lie within D
+  bool ok[NI];  // the lane's head exists and its pieces lie within D
   __device__ __forceinline__ NormLane(const NormArgs& a, const NormSplit& s) {
     const int group = threadIdx.x / LANES;
     sub = threadIdx.x % LANES;
@@ -168,90 +196,130 @@ struct NormLane {
     first_head = (int)(blockIdx.x % (unsigned)s.heads_of_blocks) * hb;
     part = (int)(blockIdx.x / (unsigned)s.heads_of_blocks);
     h = first_head + group % hb;
-    head = h < a.H;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) ok[i] = head && (i * LANES + sub) * V < a.D;
+    for (int i = 0; i < NI; ++i) ok[i] = h < a.H && (i * LANES + sub) * V < a.D;
   }
-  __device__ __forceinline__ void weights(const NormArgs& a, const float* w, float fill, float* f) const {
+  __device__ __forceinline__ void weights(const NormArgs& a, const float* w, F2* f) const {
     const float* p = w + (a.per_channel ? (int64_t)h * a.D : 0);
+    float flat[2 * E] = {};
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (w && ok[i]) flat[i * V + v] = p[(i * LANES + sub) * V + v];
+    }
+    pack(flat, f);
+  }
+  static __device__ __forceinline__ void pack(const float* flat, F2* f) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = f2(flat[2 * e], flat[2 * e + 1]);
+  }
+  static __device__ __forceinline__ void unpack(const F2* f, float* flat) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f2_get(f[e], flat[2 * e], flat[2 * e + 1]);
+  }
+  // array n of the row, 0 where there is none
+  static __device__ __forceinline__ void get(const P& pieces, int n, F2* f) {
+    float flat[2 * E] = {};
 #pragma unroll
     for (int i = 0; i < NI; ++i)
+      pieces.get(n, i, flat + i * V);
+    pack(flat, f);
+  }
+  template <typename Act>
+  __device__ __forceinline__ void put(Act* p, bool live, const F2* f) const {
+    float flat[2 * E];
+    unpack(f, flat);
 #pragma unroll
-      for (int v = 0; v < V; ++v) f[i * V + v] = w && ok[i] ? p[(i * LANES + sub) * V + v] : fill;
+    for (int i = 0; i < NI; ++i)
+      if (live && ok[i]) piece_put<Act, V>(p + i * LANES * V, flat + i * V);
   }
   // x <- n (0 where there is no channel); returns 1 / sqrt(variance + eps)
-  __device__ __forceinline__ float normalise(const NormArgs& a, float* x) const {
+  __device__ __forceinline__ float normalise(const NormArgs& a, F2* x) const {
     if (a.center) {
-      float s = 0.0f;
+      F2 s = x[0];
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += x[e];
-      const float m = lanes_sum<LANES>(s) * a.inv_d;
+      for (int e = 1; e < E; ++e) s = f2_add(s, x[e]);
+      const float m = -lanes_sum<LANES>(f2_sum(s)) * a.inv_d;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = ok[e / V] ? x[e] - m : 0.0f;
+      for (int e = 0; e < E; ++e) {
+        constexpr int last = NI * V - 1;
+        x[e] = f2_add(x[e], f2(ok[2 * e / V] ? m : 0.0f,
+                               2 * e < last && ok[(2 * e < last ? 2 * e + 1 : 0) / V] ? m : 0.0f));
+      }
     }
-    float s = 0.0f;
+    F2 s = f2_mul(x[0], x[0]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(x[e], x[e], s);
-    const float var = fmaf(lanes_sum<LANES>(s), a.inv_d, a.eps);
-    const float rstd = rsqrtf(var);
+    for (int e = 1; e < E; ++e) s = f2_fma(x[e], x[e], s);
+    const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(f2_sum(s)), a.inv_d, a.eps));
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] *= rstd;
+    for (int e = 0; e < E; ++e) x[e] = f2_mul(x[e], f2_all(rstd));
     return rstd;
   }
 };
 
-template <typename Act, bool GATE, class P>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a, NormSplit split) {
-  constexpr int N = GATE ? 2 : 1, NI = P::NI, V = P::V, E = NI * V;
+// Calls f with the activation as a constant: one uniform branch per row.
+template <class F>
+__device__ __forceinline__ void with_activation(int activation, F f) {
+  if (activation == GDN_ACT_SILU)
+    f(std::integral_constant<int, GDN_ACT_SILU>());
+  else if (activation == GDN_ACT_SIGMOID)
+    f(std::integral_constant<int, GDN_ACT_SIGMOID>());
+  else
+    f(std::integral_constant<int, GDN_ACT_NONE>());
+}
+
+template <typename Act, bool GATE, class P, int MINB>
+__global__ void __launch_bounds__(kNormThreads, MINB) norm_kernel(NormArgs a, NormSplit split) {
+  using Lane = NormLane<P>;
+  constexpr int N = GATE ? 2 : 1, NI = P::NI, V = P::V, E = Lane::E;
   extern __shared__ __align__(128) uint8_t rings[];
-  const NormLane<P> q(a, split);
-  float w[E], bias[E];
-  q.weights(a, a.w, 0.0f, w);
-  q.weights(a, a.bias, 0.0f, bias);
+  const Lane q(a, split);
+  F2 w[E], bias[E];
+  q.weights(a, a.w, w);
+  q.weights(a, a.bias, bias);
   P pieces(rings);
   const int64_t tokens = (int64_t)a.B * a.L, step = (int64_t)split.parts * q.tb;
   const int64_t first = (int64_t)q.part * q.tb, mine = threadIdx.x / P::LANES >> split.hb_log;
   Walk ahead(first + mine, step, tokens, a.L), at = ahead;
+  Offset<Act> x_at(a.x, ahead, q.h, q.sub * V, a.L), z_at(a.z, ahead, q.h, q.sub * V, a.L);
+  Offset<Act> y_at(a.y, at, q.h, q.sub * V, a.L);
   auto fetch = [&]() {
-    const bool live = ahead.left > 0 && ahead.l < seq_len(a.lens, ahead.b, a.L);
+    const bool live = ahead.live(a.lens, a.L);
     bool there[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) there[i] = live && q.ok[i];
-    const Act* from[N];
-    from[0] = static_cast<const Act*>(a.x.p) + row_offset(a.x, ahead.b, ahead.l, q.h) + q.sub * V;
-    if constexpr (GATE)
-      from[1] = static_cast<const Act*>(a.z.p) + row_offset(a.z, ahead.b, ahead.l, q.h) + q.sub * V;
-    pieces.fetch(from, there);
+    const Act *from[N], *base[N];
+    from[0] = x_at.p, base[0] = static_cast<const Act*>(a.x.p);
+    if constexpr (GATE) from[1] = z_at.p, base[1] = static_cast<const Act*>(a.z.p);
+    pieces.fetch(from, base, there);
     ahead.next(a.L);
+    x_at.next(ahead);
+    if constexpr (GATE) z_at.next(ahead);
   };
 #pragma unroll
   for (int i = 0; i < P::kAhead; ++i) fetch();
-  for (int64_t t = first; t < tokens; t += step, at.next(a.L)) {
+  for (int64_t t = first; t < tokens; t += step) {
     pieces.wait();
-    const bool live = at.left > 0 && at.l < seq_len(a.lens, at.b, a.L);
-    float x[E], z[E];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (live && q.ok[i]) {
-        pieces.get(0, i, x + i * V);
-        if constexpr (GATE) pieces.get(1, i, z + i * V);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[i * V + v] = z[i * V + v] = 0.0f;
-      }
-    }
+    const bool live = at.live(a.lens, a.L);
+    F2 x[E], z[E];
+    Lane::get(pieces, 0, x);
+    if constexpr (GATE) Lane::get(pieces, 1, z);
     pieces.done();
     fetch();
     q.normalise(a, x);
+    with_activation(a.activation, [&](auto act) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float u = fmaf(x[e], w[e], bias[e]);
-      x[e] = GATE ? u * act_slope(a.activation, z[e]).x : act_slope(a.activation, u).x;
-    }
-    Act* y = static_cast<Act*>(a.y.p) + row_offset(a.y, at.b, at.l, q.h) + q.sub * V;
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (live && q.ok[i]) piece_put<Act, V>(y + i * P::LANES * V, x + i * V);
+      for (int e = 0; e < E; ++e) {
+        const F2 u = f2_fma(x[e], w[e], bias[e]);
+        F2 v, slope;
+        act_pair<decltype(act)::value, false>(GATE ? z[e] : u, v, slope);
+        x[e] = GATE ? f2_mul(u, v) : v;
+      }
+    });
+    q.put(y_at.p, live, x);
+    at.next(a.L);
+    y_at.next(at);
   }
 }
 
@@ -264,90 +332,91 @@ constexpr int norm_backward_shared() {
 
 // Leaves its sums of du n and du at partials[CTA][2][D] (weights shared by the heads) or
 // partials[part][head][2][D].
-template <typename Act, bool GATE, class P>
-__global__ void __launch_bounds__(kNormThreads, P::NI * P::V <= 16 ? 2 : 1) norm_backward_kernel(NormArgs a, NormSplit split) {
-  constexpr int N = GATE ? 3 : 2, NI = P::NI, V = P::V, E = NI * V, LANES = P::LANES;
+template <typename Act, bool GATE, class P, int MINB>
+__global__ void __launch_bounds__(kNormThreads, MINB) norm_backward_kernel(NormArgs a, NormSplit split) {
+  using Lane = NormLane<P>;
+  constexpr int N = GATE ? 3 : 2, NI = P::NI, V = P::V, E = Lane::E, LANES = P::LANES;
   extern __shared__ __align__(128) uint8_t rings[];
-  const NormLane<P> q(a, split);
-  float w[E], bias[E], sw[E], sb[E];
-  q.weights(a, a.w, 0.0f, w);
-  q.weights(a, a.bias, 0.0f, bias);
+  const Lane q(a, split);
+  F2 w[E], bias[E], sw[E], sb[E];
+  q.weights(a, a.w, w);
+  q.weights(a, a.bias, bias);
 #pragma unroll
-  for (int e = 0; e < E; ++e) sw[e] = sb[e] = 0.0f;
+  for (int e = 0; e < E; ++e) sw[e] = sb[e] = f2_all(0.0f);
   P pieces(rings);
   const int64_t tokens = (int64_t)a.B * a.L, step = (int64_t)split.parts * q.tb;
   const int64_t first = (int64_t)q.part * q.tb, mine = threadIdx.x / LANES >> split.hb_log;
   Walk ahead(first + mine, step, tokens, a.L), at = ahead;
+  Offset<Act> x_at(a.x, ahead, q.h, q.sub * V, a.L), z_at(a.z, ahead, q.h, q.sub * V, a.L);
+  Offset<Act> dy_at(a.grad_y, ahead, q.h, q.sub * V, a.L);
+  Offset<Act> dx_at(a.grad_x, at, q.h, q.sub * V, a.L), dz_at(a.grad_z, at, q.h, q.sub * V, a.L);
   auto fetch = [&]() {
-    const bool live = ahead.left > 0 && ahead.l < seq_len(a.lens, ahead.b, a.L);
+    const bool live = ahead.live(a.lens, a.L);
     bool there[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) there[i] = live && q.ok[i];
-    const Act* from[N];
-    from[0] = static_cast<const Act*>(a.x.p) + row_offset(a.x, ahead.b, ahead.l, q.h) + q.sub * V;
-    from[1] = static_cast<const Act*>(a.grad_y.p) + row_offset(a.grad_y, ahead.b, ahead.l, q.h) + q.sub * V;
-    if constexpr (GATE)
-      from[2] = static_cast<const Act*>(a.z.p) + row_offset(a.z, ahead.b, ahead.l, q.h) + q.sub * V;
-    pieces.fetch(from, there);
+    const Act *from[N], *base[N];
+    from[0] = x_at.p, base[0] = static_cast<const Act*>(a.x.p);
+    from[1] = dy_at.p, base[1] = static_cast<const Act*>(a.grad_y.p);
+    if constexpr (GATE) from[2] = z_at.p, base[2] = static_cast<const Act*>(a.z.p);
+    pieces.fetch(from, base, there);
     ahead.next(a.L);
+    x_at.next(ahead);
+    dy_at.next(ahead);
+    if constexpr (GATE) z_at.next(ahead);
   };
 #pragma unroll
   for (int i = 0; i < P::kAhead; ++i) fetch();
-  for (int64_t t = first; t < tokens; t += step, at.next(a.L)) {
+  for (int64_t t = first; t < tokens; t += step) {
     pieces.wait();
-    const bool live = at.left > 0 && at.l < seq_len(a.lens, at.b, a.L);
-    float x[E], dy[E], z[E];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (live && q.ok[i]) {
-        pieces.get(0, i, x + i * V);
-        pieces.get(1, i, dy + i * V);
-        if constexpr (GATE) pieces.get(2, i, z + i * V);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[i * V + v] = dy[i * V + v] = z[i * V + v] = 0.0f;
-      }
-    }
+    const bool live = at.live(a.lens, a.L);
+    F2 x[E], dy[E], z[E];
+    Lane::get(pieces, 0, x);
+    Lane::get(pieces, 1, dy);
+    if constexpr (GATE) Lane::get(pieces, 2, z);
     pieces.done();
     fetch();
     const float rstd = q.normalise(a, x);
-    float s1 = 0.0f, s2 = 0.0f;
+    F2 s1 = f2_all(0.0f), s2 = s1;
+    with_activation(a.activation, [&](auto act) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float u = fmaf(x[e], w[e], bias[e]);
-      const float2 f = act_slope(a.activation, GATE ? z[e] : u);
-      const float du = dy[e] * (GATE ? f.x : f.y);
-      if constexpr (GATE) z[e] = dy[e] * u * f.y;  // grad_z
-      sw[e] = fmaf(du, x[e], sw[e]);
-      sb[e] += du;
-      dy[e] = du * w[e];  // dn
-      s1 += dy[e];
-      s2 = fmaf(dy[e], x[e], s2);
-    }
-    const float m1 = a.center ? lanes_sum<LANES>(s1) * a.inv_d : 0.0f;
-    const float m2 = lanes_sum<LANES>(s2) * a.inv_d;
-#pragma unroll
-    for (int e = 0; e < E; ++e) dy[e] = (dy[e] - fmaf(x[e], m2, m1)) * rstd;
-    Act* gx = static_cast<Act*>(a.grad_x.p) + row_offset(a.grad_x, at.b, at.l, q.h) + q.sub * V;
-    Act* gz = nullptr;
-    if constexpr (GATE)
-      gz = static_cast<Act*>(a.grad_z.p) + row_offset(a.grad_z, at.b, at.l, q.h) + q.sub * V;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (live && q.ok[i]) {
-        piece_put<Act, V>(gx + i * LANES * V, dy + i * V);
-        if constexpr (GATE) piece_put<Act, V>(gz + i * LANES * V, z + i * V);
+      for (int e = 0; e < E; ++e) {
+        const F2 u = f2_fma(x[e], w[e], bias[e]);
+        F2 v, slope;
+        act_pair<decltype(act)::value, true>(GATE ? z[e] : u, v, slope);
+        const F2 du = f2_mul(dy[e], GATE ? v : slope);
+        if constexpr (GATE) z[e] = f2_mul(f2_mul(dy[e], u), slope);  // grad_z
+        sw[e] = f2_fma(du, x[e], sw[e]);
+        sb[e] = f2_add(sb[e], du);
+        dy[e] = f2_mul(du, w[e]);  // dn
+        s1 = f2_add(s1, dy[e]);
+        s2 = f2_fma(dy[e], x[e], s2);
       }
-    }
+    });
+    const float m1 = a.center ? lanes_sum<LANES>(f2_sum(s1)) * a.inv_d : 0.0f;
+    const float m2 = lanes_sum<LANES>(f2_sum(s2)) * a.inv_d;
+    // rstd (dn - m1 - n m2)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      dy[e] = f2_fma(dy[e], f2_all(rstd), f2_mul(f2_fma(x[e], f2_all(m2), f2_all(m1)), f2_all(-rstd)));
+    q.put(dx_at.p, live, dy);
+    if constexpr (GATE) q.put(dz_at.p, live, z);
+    at.next(a.L);
+    dx_at.next(at);
+    if constexpr (GATE) dz_at.next(at);
   }
   // the CTA's sums, rows in order; the ring is no longer read, but copies may still be landing
   asm volatile("cp.async.wait_all;\n" ::: "memory");
   __syncthreads();
   float2* sums = reinterpret_cast<float2*>(rings);  // [row of the CTA][channel]
-  constexpr int kWide = LANES * E, kRows = kNormThreads / LANES;
+  constexpr int kWide = LANES * NI * V, kRows = kNormThreads / LANES;
+  float flat_w[2 * E], flat_b[2 * E];
+  Lane::unpack(sw, flat_w);
+  Lane::unpack(sb, flat_b);
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    sums[threadIdx.x / LANES * kWide + (e / V * LANES + q.sub) * V + e % V] = make_float2(sw[e], sb[e]);
+  for (int c = 0; c < NI * V; ++c)
+    sums[threadIdx.x / LANES * kWide + (c / V * LANES + q.sub) * V + c % V] =
+        make_float2(flat_w[c], flat_b[c]);
   __syncthreads();
   const int keep = a.per_channel ? q.hb : 1;  // sums that stay apart
   for (int i = threadIdx.x; i < keep * a.D; i += kNormThreads) {

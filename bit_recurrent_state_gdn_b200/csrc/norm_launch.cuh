@@ -6,12 +6,20 @@
 #include "norm_kernels.cuh"
 #include "window_dispatch.cuh"
 
+#ifndef NF
+#define NF 3
+#define SF 4
+#endif
+#ifndef NB
+#define NB 2
+#define SB 4
+#endif
 namespace gdnq {
 
 // The lanes of a row, the heads of a CTA and the CTAs of a launch. Heads side by side make a
 // token's reads at least 512 bytes long where the heads allow it without idle lanes, and 128 with
 // them. CTAs: three per SM, the tokens shared out evenly over them.
-inline NormSplit norm_plan(int D, int H, int64_t tokens, int elem, int lanes) {
+inline NormSplit norm_plan(int D, int H, int64_t tokens, int elem, int lanes, int resident) {
   NormSplit s;
   s.lanes = lanes;
   const int rows = kNormThreads / lanes;
@@ -22,7 +30,7 @@ inline NormSplit norm_plan(int D, int H, int64_t tokens, int elem, int lanes) {
   s.hb_log = log;
   s.heads_of_blocks = (H + hb - 1) / hb;
   const int64_t tb = rows / hb, most = (tokens + tb - 1) / tb;
-  s.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, 444 / s.heads_of_blocks));
+  s.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, 148 * resident / s.heads_of_blocks));
   return s;
 }
 
@@ -46,22 +54,29 @@ inline int64_t norm_partials(const NormSplit& s, int H, bool per_channel) {
 
 cudaError_t launch_norm_reduce(const NormArgs& a, int64_t partials, cudaStream_t st);
 
+// CTAs per SM that the kernels' registers are bounded for, by the channels that a lane holds.
+constexpr int norm_resident(int channels, bool backward) {
+  return backward ? (channels <= 8 ? NB : channels <= 16 ? 2 : 1) : (channels <= 8 ? NF : 2);
+}
+
 template <typename Act, bool GATE, class F, class B>
 cudaError_t norm_go(const NormArgs& a, bool backward, cudaStream_t st) {
   const int64_t tokens = (int64_t)a.B * a.L;
   if (!backward) {
-    constexpr auto kernel = norm_kernel<Act, GATE, F>;
+    constexpr int kResident = norm_resident(F::NI * F::V, false);
+    constexpr auto kernel = norm_kernel<Act, GATE, F, kResident>;
     cudaError_t e = ensure_smem<kernel>(F::kBytes);
     if (e != cudaSuccess) return e;
-    const NormSplit s = norm_plan(a.D, a.H, tokens, sizeof(Act), F::LANES);
+    const NormSplit s = norm_plan(a.D, a.H, tokens, sizeof(Act), F::LANES, kResident);
     kernel<<<(unsigned)s.parts * (unsigned)s.heads_of_blocks, kNormThreads, F::kBytes, st>>>(a, s);
     return cudaGetLastError();
   }
-  constexpr auto kernel = norm_backward_kernel<Act, GATE, B>;
+  constexpr int kResident = norm_resident(B::NI * B::V, true);
+  constexpr auto kernel = norm_backward_kernel<Act, GATE, B, kResident>;
   constexpr int kShared = norm_backward_shared<B>();
   cudaError_t e = ensure_smem<kernel>(kShared);
   if (e != cudaSuccess) return e;
-  const NormSplit s = norm_plan(a.D, a.H, tokens, sizeof(Act), B::LANES);
+  const NormSplit s = norm_plan(a.D, a.H, tokens, sizeof(Act), B::LANES, kResident);
   kernel<<<(unsigned)s.parts * (unsigned)s.heads_of_blocks, kNormThreads, kShared, st>>>(a, s);
   e = cudaGetLastError();
   return e == cudaSuccess ? launch_norm_reduce(a, norm_partials(s, a.H, a.per_channel), st) : e;
@@ -70,8 +85,8 @@ cudaError_t norm_go(const NormArgs& a, bool backward, cudaStream_t st) {
 template <typename Act, bool GATE, int LANES, int NI>
 cudaError_t norm_ring(const NormArgs& a, bool backward, cudaStream_t st) {
   constexpr int kF = GATE ? 2 : 1, kB = kF + 1;
-  return norm_go<Act, GATE, PiecesInShared<Act, LANES, NI, kF, NI == 1 ? 6 : NI == 2 ? 4 : NI == 4 ? 3 : 2>,
-                 PiecesInShared<Act, LANES, NI, kB, NI == 1 ? 4 : NI == 2 ? 3 : 2>>(a, backward, st);
+  return norm_go<Act, GATE, PiecesInShared<Act, LANES, NI, kF, NI == 1 ? SF : NI == 2 ? 4 : NI == 4 ? 3 : 2>,
+                 PiecesInShared<Act, LANES, NI, kB, NI == 1 ? SB : NI == 2 ? 3 : 2>>(a, backward, st);
 }
 
 template <typename Act, bool GATE, int LANES, int NI>

@@ -23,8 +23,6 @@ struct Gate {
   F2 r;     // 1 / s of GDN_SCALE_SQRT, 0 where s is 0 (backward pass)
 };
 
-__device__ __forceinline__ F2 f2_all(float x) { return f2(x, x); }
-
 // e^g and 1 - e^g. Near zero e^g - 1 = g p(g), p of degree 5 through the Chebyshev points of
 // [-0.35, 0.35], off by at most 2.6e-8 of itself (half an fp32 step is 6.0e-8), so that neither
 // 1 - e^g nor a gate near one loses digits; elsewhere by the hardware's exponential, which takes

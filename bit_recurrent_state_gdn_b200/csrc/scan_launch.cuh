@@ -153,7 +153,7 @@ cudaError_t launch_scan_scale(ScanArgs a, bool backward, cudaStream_t st) {
     a.H = 1;
     a.x.sh = a.g.sh = a.o.sh = a.grad_o.sh = a.grad_x.sh = a.grad_g.sh = 0;
   }
-  bool pairs = true, pieces = true;
+  bool pairs = true, pieces = a.L > 0;
   for (const Used& u : read) {
     pairs = pairs && aligned(*u.t, a.D, 2, u.elem);
     pieces = pieces && aligned(*u.t, a.D, (int)(16 / u.elem), u.elem);
