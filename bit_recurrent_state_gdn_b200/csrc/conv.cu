@@ -4,19 +4,19 @@
 namespace gdnq {
 namespace {
 
-// grad_w [C][K] and grad_bias [C] from partials[parts][K + 1][C]: a CTA takes 32 sums, its 32
-// warps every 32nd part, added in the same order every time.
-__global__ void __launch_bounds__(1024) conv_reduce_kernel(ConvArgs a, int parts) {
-  __shared__ float sum[32][33];
+// grad_w [C][K] and grad_bias [C] from partials[parts][K + 1][C]: a CTA takes 32 sums, its 8
+// warps every 8th part, added in the same order every time.
+__global__ void __launch_bounds__(256) conv_reduce_kernel(ConvArgs a, int parts) {
+  __shared__ float sum[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = (int64_t)a.C * (a.K + 1), i = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (i < n)
-    for (int p = warp; p < parts; p += 32) s += a.partials[p * n + i];
+    for (int p = warp; p < parts; p += 8) s += a.partials[p * n + i];
   sum[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && i < n) {
-    for (int w = 1; w < 32; ++w) s += sum[w][lane];
+    for (int w = 1; w < 8; ++w) s += sum[w][lane];
     const int64_t c = i % a.C;
     const int j = (int)(i / a.C);
     if (j < a.K)
@@ -30,14 +30,14 @@ __global__ void __launch_bounds__(1024) conv_reduce_kernel(ConvArgs a, int parts
 
 cudaError_t launch_conv_reduce(const ConvArgs& a, int parts, cudaStream_t st) {
   const int64_t n = (int64_t)a.C * (a.K + 1);
-  conv_reduce_kernel<<<(unsigned)((n + 31) / 32), 1024, 0, st>>>(a, parts);
+  conv_reduce_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(a, parts);
   return cudaGetLastError();
 }
 
 // Large enough for any placement of the arrays, on which the split depends.
 size_t conv_backward_workspace(const gdn_conv_config& cfg, int L) {
   const int C = cfg.H * cfg.D;
-  const int parts = std::max(conv_backward_split(cfg.B, L, C, 4).parts,
+  const int parts = std::max(conv_backward_split(cfg.B, L, C, kConvBackVec).parts,
                              conv_backward_split(cfg.B, L, C, 1).parts);
   return (size_t)parts * (size_t)C * (size_t)(cfg.K + 1) * sizeof(float);
 }

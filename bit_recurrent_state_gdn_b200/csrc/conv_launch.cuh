@@ -6,64 +6,70 @@
 #include "conv_kernels.cuh"
 #include "window_dispatch.cuh"
 
-#ifndef CF
-#define CF 2
-#define VF 16
-#define CSF 3
-#define CWAVE 1
-#define CDEC 1
-#endif
-#ifndef CB
-#define CB 2
-#define CSB 3
-#define CBK 1
-#endif
 namespace gdnq {
 
-// Tokens of a run at least: the K - 1 tokens before it are read twice.
-constexpr int kConvRun = 16;
+// CTAs per SM that the kernels' registers are bounded for. Three of the run kernels spill (8 x 4096
+// channels x 4096 tokens forward 107 us against 96; backward 4 sequences 220 against 95).
+constexpr int kConvResident = 2, kConvStepResident = 4;
+// Channels of a thread backward (with 2: 125 us against 95), and for one token, whose K rows of
+// several sequences are in registers (8 channels: 18.4 us against 16.3, 1024 x 4096 channels).
+constexpr int kConvBackVec = 4, kConvStepVec = 4;
 
-inline ConvSplit conv_runs(int B, int L, int columns, int64_t threads) {
+// Tokens of a run at least: the K - 1 tokens before it (backward, also behind it) are read twice.
+constexpr int kConvRun = 32;
+
+inline ConvSplit conv_split(int B, int L, int columns, int64_t threads) {
   ConvSplit s;
   s.columns = columns;
-  const int64_t want = std::max<int64_t>(1, threads / std::max<int64_t>(1, (int64_t)B * columns));
-  const int64_t most = std::max<int64_t>(1, L / kConvRun);
-  const int64_t runs = std::min(want, most);
+  const int64_t runs = std::min(shares(threads, std::max<int64_t>(1, (int64_t)B * columns)),
+                                std::max<int64_t>(1, L / kConvRun));
   s.run_tokens = (int)std::max<int64_t>(1, (L + runs - 1) / runs);
   s.runs = (int)std::max<int64_t>(1, ((int64_t)L + s.run_tokens - 1) / s.run_tokens);
-  s.parts = 1;
-  return s;
-}
-
-inline ConvSplit conv_forward_split(int B, int L, int columns) {
-  const int64_t threads = (int64_t)148 * CF * kConvThreads * (L < 8 ? CDEC : CWAVE);
-  ConvSplit s = conv_runs(B, L, columns, threads);
   s.parts = (int)std::min<int64_t>((int64_t)B * s.runs, std::max<int64_t>(1, threads / columns));
   return s;
 }
 
 inline ConvSplit conv_backward_split(int B, int L, int C, int V) {
+  constexpr int kRows = kConvThreads / 32;
   const int columns = (C + V - 1) / V, slabs = (columns + 31) / 32;
-  const int64_t parts = std::max(1, 148 * CB / slabs), rows = parts * (kConvThreads / 32);
-  ConvSplit s = conv_runs(B, L, columns, rows * columns * CBK);
-  s.parts = (int)std::min<int64_t>(parts, ((int64_t)B * s.runs + kConvThreads / 32 - 1) / (kConvThreads / 32));
+  const int64_t parts = std::max(1, kSms * kConvResident / slabs);
+  ConvSplit s = conv_split(B, L, columns, parts * kRows * columns);
+  s.parts = (int)std::min<int64_t>(parts, ((int64_t)B * s.runs + kRows - 1) / kRows);
   return s;
 }
 
 cudaError_t launch_conv_reduce(const ConvArgs& a, int parts, cudaStream_t st);
 
-template <typename Act, int K, bool SILU, class F, class B>
+template <int N>
+struct StepVec {
+  static constexpr int V = N;
+};
+
+template <typename Act, int K, bool SILU, class F, class B, class S>
 cudaError_t conv_go(const ConvArgs& a, bool backward, cudaStream_t st) {
+  if (!backward && a.L == 1) {
+    // a thread takes several sequences where there are more than fill the machine
+    const ConvSplit s = conv_split(a.B, 1, (a.C + S::V - 1) / S::V,
+                                   (int64_t)kSms * kConvStepResident * kConvThreads);
+    const int64_t threads = (int64_t)s.parts * s.columns;
+    const unsigned grid = (unsigned)((threads + kConvThreads - 1) / kConvThreads);
+    if (s.parts == a.B)
+      conv_step_kernel<Act, K, SILU, S::V, 1, kConvStepResident><<<grid, kConvThreads, 0, st>>>(a, s);
+    else
+      conv_step_kernel<Act, K, SILU, S::V, 2, kConvStepResident><<<grid, kConvThreads, 0, st>>>(a, s);
+    return cudaGetLastError();
+  }
   if (!backward) {
-    constexpr auto kernel = conv_kernel<Act, K, SILU, F, CF>;
+    constexpr auto kernel = conv_kernel<Act, K, SILU, F, kConvResident>;
     const cudaError_t e = ensure_smem<kernel>(F::kBytes);
     if (e != cudaSuccess) return e;
-    const ConvSplit s = conv_forward_split(a.B, a.L, (a.C + F::V - 1) / F::V);
+    const ConvSplit s = conv_split(a.B, a.L, (a.C + F::V - 1) / F::V,
+                                   (int64_t)kSms * kConvResident * kConvThreads);
     const int64_t threads = (int64_t)s.parts * s.columns;
     kernel<<<(unsigned)((threads + kConvThreads - 1) / kConvThreads), kConvThreads, F::kBytes, st>>>(a, s);
     return cudaGetLastError();
   }
-  constexpr auto kernel = conv_backward_kernel<Act, K, SILU, B, 32, CB>;
+  constexpr auto kernel = conv_backward_kernel<Act, K, SILU, B, 32, kConvResident>;
   constexpr int kShared = conv_backward_shared<K, 32, B>();
   cudaError_t e = ensure_smem<kernel>(kShared);
   if (e != cudaSuccess) return e;
@@ -74,18 +80,24 @@ cudaError_t conv_go(const ConvArgs& a, bool backward, cudaStream_t st) {
   return e == cudaSuccess ? launch_conv_reduce(a, s.parts, st) : e;
 }
 
+// `wide` channels may be moved as one: vectors of them, pairs, or single channels.
 template <typename Act, int K, bool SILU>
-cudaError_t conv_by_place(const ConvArgs& a, bool backward, bool pieces, cudaStream_t st) {
-  if (pieces)
-    return conv_go<Act, K, SILU, RowsInShared<Act, VF / (int)sizeof(Act), K, 1, CSF>,
-                   RowsInShared<Act, 4, K, 2, CSB>>(a, backward, st);
-  return conv_go<Act, K, SILU, RowsInRegisters<Act, K, 1>, RowsInRegisters<Act, K, 2>>(a, backward, st);
+cudaError_t conv_by_place(const ConvArgs& a, bool backward, int wide, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(Act);
+  if (wide >= (backward ? kConvBackVec : V))
+    return conv_go<Act, K, SILU, RowsInShared<Act, V, K, 1, 3>, RowsInShared<Act, kConvBackVec, K, 2, 3>,
+                   StepVec<kConvStepVec>>(a, backward, st);
+  if (wide >= 2)
+    return conv_go<Act, K, SILU, RowsInShared<Act, 2, K, 1, 4>, RowsInShared<Act, 2, K, 2, 3>,
+                   StepVec<2>>(a, backward, st);
+  return conv_go<Act, K, SILU, RowsInRegisters<Act, K, 1>, RowsInRegisters<Act, K, 2>, StepVec<1>>(
+      a, backward, st);
 }
 
 template <typename Act, int K>
-cudaError_t conv_by_act(const ConvArgs& a, bool backward, bool pieces, cudaStream_t st) {
-  return a.activation == GDN_ACT_SILU ? conv_by_place<Act, K, true>(a, backward, pieces, st)
-                                      : conv_by_place<Act, K, false>(a, backward, pieces, st);
+cudaError_t conv_by_act(const ConvArgs& a, bool backward, int wide, cudaStream_t st) {
+  return a.activation == GDN_ACT_SILU ? conv_by_place<Act, K, true>(a, backward, wide, st)
+                                      : conv_by_place<Act, K, false>(a, backward, wide, st);
 }
 
 template <typename Act>
@@ -100,20 +112,22 @@ cudaError_t launch_conv_as(ConvArgs a, bool backward, cudaStream_t st) {
     a.H = 1;
     a.x.sh = a.y.sh = a.grad_y.sh = a.grad_x.sh = 0;
   }
-  // vectors of V channels in one head, aligned: 16 bytes, backward those of 4 channels
-  const int V = backward ? 4 : VF / (int)sizeof(Act);
-  bool pieces = a.L > 0 && a.D % V == 0;
-  for (const Tok* t : used)
-    pieces = pieces && t->sb % V == 0 && t->sl % V == 0 && t->sh % V == 0 &&
-             reinterpret_cast<uintptr_t>(t->p) % (V * sizeof(Act)) == 0;
-  for (const void* s : states) pieces = pieces && reinterpret_cast<uintptr_t>(s) % (V * sizeof(Act)) == 0;
+  // the most channels that lie in one head and are aligned wherever they begin
+  int wide = a.L > 0 ? 16 / (int)sizeof(Act) : 1;
+  for (bool fits = false; !fits && wide > 1; wide /= fits ? 1 : 2) {
+    fits = a.D % wide == 0;
+    for (const Tok* t : used)
+      fits = fits && t->sb % wide == 0 && t->sl % wide == 0 && t->sh % wide == 0 &&
+             reinterpret_cast<uintptr_t>(t->p) % (wide * sizeof(Act)) == 0;
+    for (const void* s : states) fits = fits && reinterpret_cast<uintptr_t>(s) % (wide * sizeof(Act)) == 0;
+  }
   switch (a.K) {
     case 2:
-      return conv_by_act<Act, 2>(a, backward, pieces, st);
+      return conv_by_act<Act, 2>(a, backward, wide, st);
     case 3:
-      return conv_by_act<Act, 3>(a, backward, pieces, st);
+      return conv_by_act<Act, 3>(a, backward, wide, st);
     default:
-      return conv_by_act<Act, 4>(a, backward, pieces, st);
+      return conv_by_act<Act, 4>(a, backward, wide, st);
   }
 }
 

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cstdint>
 
 #include "gdnq_layer.h"
 
@@ -53,6 +54,16 @@ struct ConvArgs {
   int B, L, H, D, C, K;
   int activation;
 };
+
+constexpr int kSms = 148;
+
+// Into how many parts each of `units` equal pieces of work goes on a machine that holds `slots`
+// parts at a time: as many as fit at once, or where fewer than four of them do (so that rounding
+// down would leave much of the machine idle) enough for four turns.
+inline int64_t shares(int64_t slots, int64_t units) {
+  const int64_t fit = slots / units;
+  return fit >= 4 ? fit : (4 * slots + units - 1) / units;
+}
 
 // Forward or backward scan, by activation type; scale is a gdn_input_scale.
 cudaError_t launch_scan_f32(const ScanArgs& a, int scale, bool backward, cudaStream_t st);

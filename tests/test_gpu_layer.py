@@ -356,6 +356,13 @@ CONV = [
     (1, 500, 2, 72, "f32", 4, True, "silu", "tokens", None),
     (40, 70, 4, 128, "bf16", 4, True, "silu", "tokens", None),
     (300, 1, 8, 128, "bf16", 4, False, "silu", "tokens", None),
+    # channels in pairs and fours, several sequences a thread, long sequences in many runs
+    (3, 70, 3, 50, "bf16", 4, True, "silu", "heads", [70, 3, 69]),
+    (2, 33, 1, 50, "f32", 3, True, "silu", "tokens", None),
+    (2, 90, 3, 20, "bf16", 4, False, "none", "heads", None),
+    (2100, 1, 16, 128, "bf16", 4, True, "silu", "tokens", [1, 1, 0] * 700),
+    (2100, 1, 3, 50, "f32", 2, False, "silu", "tokens", None),
+    (1, 5000, 1, 64, "bf16", 4, True, "silu", "tokens", None),
 ]
 
 
