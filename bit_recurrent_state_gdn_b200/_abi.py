@@ -86,7 +86,7 @@ class gdn_conv_config(ctypes.Structure):
     _fields_ = [(n, _i32) for n in ("B", "H", "D", "K", "activation", "act_dtype")]
 
 
-_TK = ctypes.POINTER(gdn_tokens)
+_TK = _vp  # const gdn_tokens*: a pointer or the structure's bytes
 _SC, _NC, _CC = (ctypes.POINTER(c) for c in (gdn_scan_config, gdn_norm_config, gdn_conv_config))
 _PWC, _PWS = ctypes.POINTER(gdn_pw_config), ctypes.POINTER(gdn_pw_state)
 

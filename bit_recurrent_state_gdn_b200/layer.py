@@ -9,13 +9,14 @@ tensors -> pointers and strides, status codes -> exceptions. Same conventions as
 """
 from __future__ import annotations
 
-from ctypes import byref
+import struct
+from ctypes import byref, sizeof
 from typing import Optional
 
 import torch
 
 from . import _abi
-from .api import _DT, _TORCH_DT, _check
+from .api import _DT, _TORCH_DT, GdnError
 
 _SCALE = {"none": _abi.GDN_SCALE_NONE, "complement": _abi.GDN_SCALE_COMPLEMENT,
           "sqrt": _abi.GDN_SCALE_SQRT}
@@ -56,72 +57,92 @@ def _shape(cfg, x: torch.Tensor):
     return (cfg.B, x.shape[1], cfg.H, cfg.D)
 
 
+# A gdn_tokens as the bytes of its fields, which cost a third of a ctypes structure to make: the
+# small calls of a decode step are bound by this layer.
+_tokens_bytes = struct.Struct("@Pqqq").pack
+assert struct.calcsize("@Pqqq") == sizeof(_abi.gdn_tokens)
+
+
+# The current stream's handle without the object around it (3.2 us of a call, on the machine the
+# decode step runs on; 0.1 us so); the public way where torch has no such function.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Args:
     """Checks the tensors of one call: all on the device of the first."""
 
-    __slots__ = ("shape", "device")
+    __slots__ = ("shape", "index", "device", "channels")
 
     def __init__(self, cfg, x):
         self.shape = _shape(cfg, x)
-        self.device = x.device
+        self.channels = cfg.D
+        self.index = x.get_device()  # -1: not on a GPU
+        self.device = x.device if self.index < 0 else None
 
     def on_device(self, t, name):
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if t.get_device() != self.index or (self.index < 0 and t.device != self.device):
+            raise ValueError(f"{name} is on {t.device}, expected "
+                             f"{self.device or torch.device('cuda', self.index)}")
 
     def tokens(self, t: Optional[torch.Tensor], name: str, dtype):
         if t is None:
             return None
         if t.shape != self.shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.shape}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
         sb, sl, sh, sd = t.stride()
-        if sd != 1 and self.shape[3] > 1:
+        if sd != 1 and self.channels > 1:
             raise ValueError(f"{name} must have contiguous channels")
-        self.on_device(t, name)
-        return byref(_abi.gdn_tokens(t.data_ptr() or None, sb, sl, sh))
+        if t.get_device() != self.index or self.index < 0:
+            self.on_device(t, name)
+        return _tokens_bytes(t.data_ptr(), sb, sl, sh)
 
     def dense(self, t: Optional[torch.Tensor], name: str, dtype, numel: int):
         if t is None:
             return None
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
         if t.numel() != numel:
             raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        self.on_device(t, name)
+        if t.get_device() != self.index or self.index < 0:
+            self.on_device(t, name)
         return t.data_ptr() or None
 
     def lens(self, t):
-        return self.dense(t, "lens", torch.int32, self.shape[0])
+        return None if t is None else self.dense(t, "lens", torch.int32, self.shape[0])
 
-    def call(self, where: str, args, stream, workspace=None, need: int = 0):
-        """The C entry point ``where`` on args, the workspace (when the call has one) and the
-        stream, with the tensors' device current."""
-        fn = getattr(_abi.load(), where)
-        if self.device.type != "cuda":
+    def call(self, where: str, args, stream, workspace=None, need: int = -1):
+        """The C entry point ``where`` on args, the workspace of ``need`` bytes (calls that have
+        one) and the stream, with the tensors' device current."""
+        if self.index < 0:
             raise ValueError(f"{where}: the tensors are on {self.device}, expected a CUDA device")
-        if self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
+        if self.index != torch.cuda.current_device():
+            with torch.cuda.device(self.index):
                 return self.call(where, args, stream, workspace, need)
         if stream is None:
-            handle = torch.cuda.current_stream().cuda_stream
+            handle = _current_stream(self.index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
-        if need:
-            if workspace is None:
+        if need >= 0:
+            if workspace is None and need > 0:
                 on = torch.cuda.ExternalStream(handle) if stream is not None else None
                 with torch.cuda.stream(on):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            self.on_device(workspace, "workspace")
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-            args += (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        elif where.endswith("_backward") and where != "gdn_gated_scan_backward":
-            args += (None, 0)
-        _check(fn(*args, handle), where)
+                    workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+            if workspace is None:
+                args += (None, 0)
+            else:
+                self.on_device(workspace, "workspace")
+                if not workspace.is_contiguous():
+                    raise ValueError("workspace must be contiguous")
+                args += (workspace.data_ptr() or None,
+                         workspace.numel() * workspace.element_size())
+        status = getattr(_abi.load(), where)(*args, handle)
+        if status:
+            raise GdnError(status, where)
 
 
 def gdn_gated_scan(cfg, x, g, o, h0=None, hT=None, hist=None, lens=None, stream=None):
