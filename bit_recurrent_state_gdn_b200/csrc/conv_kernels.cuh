@@ -104,22 +104,18 @@ struct RowsInShared {
   }
   __device__ __forceinline__ void fetch() {
     const uint32_t to = ring + (uint32_t)(fill * N * K * kSlot);
+    const bool whole = t + K <= end;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const Act* row = p[n] + t * sl[n];
+      if (whole) {
 #pragma unroll
-      for (int j = 0; j < K; ++j, row += sl[n]) {
-        const bool ok = t + j < end;
-        const Act* from = ok ? row : p[n];
-        const uint32_t at = to + (uint32_t)((n * K + j) * kSlot);
-        if constexpr (kPiece == 16)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(from),
-                       "r"(ok ? 16 : 0)
-                       : "memory");
-        else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;\n" ::"r"(at), "l"(from),
-                       "r"(ok ? kPiece : 0), "n"(kPiece)
-                       : "memory");
+        for (int j = 0; j < K; ++j, row += sl[n])
+          async_piece<kPiece>(to + (uint32_t)((n * K + j) * kSlot), row);
+      } else {
+#pragma unroll
+        for (int j = 0; j < K; ++j, row += sl[n])
+          async_piece<kPiece>(to + (uint32_t)((n * K + j) * kSlot), t + j < end ? row : p[n], t + j < end);
       }
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");

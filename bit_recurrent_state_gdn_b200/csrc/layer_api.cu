@@ -151,8 +151,10 @@ gdnq::NormArgs norm_args(const gdn_norm_config* c, int32_t L) {
 
 cudaError_t launch_norm(const gdnq::NormArgs& a, const gdn_norm_config* c, bool backward,
                         gdn_stream_t stream) {
-  return c->act_dtype == GDN_DTYPE_F32 ? gdnq::launch_norm_f32(a, backward, (cudaStream_t)stream)
-                                       : gdnq::launch_norm_bf16(a, backward, (cudaStream_t)stream);
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (c->act_dtype == GDN_DTYPE_F32)
+    return backward ? gdnq::launch_norm_f32_backward(a, st) : gdnq::launch_norm_f32_forward(a, st);
+  return backward ? gdnq::launch_norm_bf16_backward(a, st) : gdnq::launch_norm_bf16_forward(a, st);
 }
 
 cudaError_t launch_conv(const gdnq::ConvArgs& a, const gdn_conv_config* c, bool backward,

@@ -68,8 +68,10 @@ inline int64_t shares(int64_t slots, int64_t units) {
 // Forward or backward scan, by activation type; scale is a gdn_input_scale.
 cudaError_t launch_scan_f32(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
 cudaError_t launch_scan_bf16(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
-cudaError_t launch_norm_f32(const NormArgs& a, bool backward, cudaStream_t st);
-cudaError_t launch_norm_bf16(const NormArgs& a, bool backward, cudaStream_t st);
+cudaError_t launch_norm_f32_forward(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_f32_backward(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_bf16_forward(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_bf16_backward(const NormArgs& a, cudaStream_t st);
 size_t norm_backward_workspace(const gdn_norm_config& cfg, int L);
 cudaError_t launch_conv_f32(const ConvArgs& a, bool backward, cudaStream_t st);
 cudaError_t launch_conv_bf16(const ConvArgs& a, bool backward, cudaStream_t st);

@@ -19,6 +19,29 @@ __device__ __forceinline__ int64_t channel_offset(const Tok& t, int b, int h, in
   return (int64_t)b * t.sb + (int64_t)h * t.sh + d;
 }
 
+// Copies BYTES (4, 8 or 16) aligned bytes to shared memory asynchronously, or zeros where `ok` does
+// not hold; `from` may be any valid address then, nothing is read.
+template <int BYTES>
+__device__ __forceinline__ void async_piece(uint32_t to, const void* from, bool ok) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(from),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;\n" ::"r"(to), "l"(from),
+                 "r"(ok ? BYTES : 0), "n"(BYTES)
+                 : "memory");
+}
+
+template <int BYTES>
+__device__ __forceinline__ void async_piece(uint32_t to, const void* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(to), "l"(from), "n"(BYTES)
+                 : "memory");
+}
+
 // 1 / sqrt(x) on the hardware path.
 __device__ __forceinline__ float rsqrt_hw(float x) {
   float y;

@@ -45,11 +45,10 @@ size_t norm_backward_workspace(const gdn_norm_config& cfg, int L) {
   const int64_t tokens = (int64_t)cfg.B * L;
   const bool per_channel = cfg.weight == GDN_WEIGHT_CHANNEL;
   int64_t most = (int64_t)norm_wide_parts(tokens, cfg.H) * cfg.H;
-  if (cfg.D <= kNormWide) {
+  if (cfg.D <= kNormWarp) {
     const int elem = cfg.act_dtype == GDN_DTYPE_F32 ? 4 : 2;
-    most = 0;
-    for (int lanes = 4; lanes <= 32; lanes *= 2)
-      most = std::max(most, norm_partials(norm_plan(cfg.D, cfg.H, tokens, elem, lanes, 3), cfg.H,
+    for (int lanes = 2; lanes <= 32; lanes *= 2)
+      most = std::max(most, norm_partials(norm_plan(cfg.D, cfg.H, tokens, elem, lanes, 2), cfg.H,
                                           per_channel));
   }
   return (size_t)most * 2 * (size_t)cfg.D * sizeof(float);

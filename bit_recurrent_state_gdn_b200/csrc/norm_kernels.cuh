@@ -39,10 +39,24 @@ __device__ __forceinline__ float2 act_slope(int activation, float u) {
 // V elements of Act at p, as floats.
 template <typename Act, int V>
 __device__ __forceinline__ void piece_get(const void* p, float* f) {
-  if constexpr (V == 1)
+  if constexpr (V == 1) {
     f[0] = Num<Act>::to_f(*static_cast<const Act*>(p));
-  else
-    Num<Act>::template load<V>(static_cast<const Act*>(p), f);
+  } else if constexpr (sizeof(Act) == 4) {
+    if constexpr (V == 4) {
+      const float4 t = *static_cast<const float4*>(p);
+      f[0] = t.x, f[1] = t.y, f[2] = t.z, f[3] = t.w;
+    } else {
+      const float2 t = *static_cast<const float2*>(p);
+      f[0] = t.x, f[1] = t.y;
+    }
+  } else {
+    uint32_t t[V / 2];
+    if constexpr (V == 8) *reinterpret_cast<uint4*>(t) = *static_cast<const uint4*>(p);
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(t) = *static_cast<const uint2*>(p);
+    if constexpr (V == 2) t[0] = *static_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) f[2 * e] = bf16_lo(t[e]), f[2 * e + 1] = bf16_hi(t[e]);
+  }
 }
 
 template <typename Act, int V>
@@ -50,16 +64,20 @@ __device__ __forceinline__ void piece_put(void* p, const float* f) {
   if constexpr (V == 1) {
     *static_cast<Act*>(p) = Num<Act>::from_f(f[0]);
   } else if constexpr (sizeof(Act) == 4) {
-    *static_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    if constexpr (V == 4)
+      *static_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+      *static_cast<float2*>(p) = make_float2(f[0], f[1]);
   } else {
-    uint4 w;
-    uint32_t* q = reinterpret_cast<uint32_t*>(&w);
+    uint32_t t[V / 2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < V / 2; ++e) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-      q[e] = *reinterpret_cast<const uint32_t*>(&h);
+      t[e] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *static_cast<uint4*>(p) = w;
+    if constexpr (V == 8) *static_cast<uint4*>(p) = *reinterpret_cast<uint4*>(t);
+    if constexpr (V == 4) *static_cast<uint2*>(p) = *reinterpret_cast<uint2*>(t);
+    if constexpr (V == 2) *static_cast<uint32_t*>(p) = t[0];
   }
 }
 
@@ -102,17 +120,17 @@ struct Offset {
 
 // The pieces of NI x LANES x V channels that one lane reads of each array of a row, N arrays.
 //
-// PiecesInShared: 16-byte pieces, S - 1 rows ahead, in slots of the lane's own.
-template <typename Act, int LANES_, int NI_, int N, int S>
+// PiecesInShared: pieces of 4, 8 or 16 aligned bytes, S - 1 rows ahead, in slots of the lane's own.
+template <typename Act, int V_, int LANES_, int NI_, int N, int S>
 struct PiecesInShared {
-  static constexpr int LANES = LANES_, NI = NI_, V = 16 / (int)sizeof(Act);
-  static constexpr int kSlot = kNormThreads * 16;
+  static constexpr int LANES = LANES_, NI = NI_, V = V_, kPiece = V * (int)sizeof(Act);
+  static constexpr int kSlot = kNormThreads * kPiece;
   static constexpr int kBytes = S * N * NI * kSlot;
   uint32_t ring;
   const uint8_t* now;
   int fill = 0, read = 0;
   __device__ __forceinline__ PiecesInShared(uint8_t* shared)
-      : ring(smem_u32(shared) + threadIdx.x * 16), now(shared + threadIdx.x * 16) {}
+      : ring(smem_u32(shared) + threadIdx.x * kPiece), now(shared + threadIdx.x * kPiece) {}
   // from[n] points at the lane's first piece of array n, ok[i] says whether piece i is there: a
   // copy of no bytes fills its slot with zeros, so that the row is read without conditions
   __device__ __forceinline__ void fetch(const Act* const (&from)[N], const Act* const (&base)[N],
@@ -122,10 +140,8 @@ struct PiecesInShared {
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                         to + (uint32_t)((n * NI + i) * kSlot)),
-                     "l"(ok[i] ? from[n] + i * LANES * V : base[n]), "r"(ok[i] ? 16 : 0)
-                     : "memory");
+        async_piece<kPiece>(to + (uint32_t)((n * NI + i) * kSlot),
+                            ok[i] ? from[n] + i * LANES * V : base[n], ok[i]);
     asm volatile("cp.async.commit_group;\n" ::: "memory");
     fill = fill + 1 == S ? 0 : fill + 1;
   }

@@ -26,14 +26,7 @@ inline NormSplit norm_plan(int D, int H, int64_t tokens, int elem, int lanes, in
   return s;
 }
 
-// Lanes for `pieces` of them per row (ring or single elements).
-inline int norm_lanes(int pieces, int fewest) {
-  int lanes = fewest;
-  while (lanes < 32 && lanes < pieces) lanes *= 2;
-  return lanes;
-}
-
-constexpr int kNormWide = 1024;  // channels of a head that a warp holds
+constexpr int kNormWarp = 1024;  // channels of a head that a warp may hold
 
 inline int norm_wide_parts(int64_t tokens, int H) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(tokens, kSms * 8 / std::max(H, 1)));
@@ -50,105 +43,117 @@ cudaError_t launch_norm_reduce(const NormArgs& a, int64_t partials, cudaStream_t
 // eight, four forward (152 us against 139, 8 x 32 x 4096 gated rows of 128) and three backward
 // (188 us against 118, four sequences) spill.
 constexpr int norm_resident(int channels, bool backward) {
-  return backward ? (channels <= 16 ? 2 : 1) : (channels <= 8 ? 3 : 2);
+  return backward ? (channels <= 8 ? 2 : 1) : (channels <= 8 ? 3 : channels <= 16 ? 2 : 1);
 }
 
-template <typename Act, bool GATE, class F, class B>
-cudaError_t norm_go(const NormArgs& a, bool backward, cudaStream_t st) {
-  const int64_t tokens = (int64_t)a.B * a.L;
-  if (!backward) {
-    constexpr int kResident = norm_resident(F::NI * F::V, false);
-    constexpr auto kernel = norm_kernel<Act, GATE, F, kResident>;
-    cudaError_t e = ensure_smem<kernel>(F::kBytes);
+template <typename Act, bool GATE, bool BACKWARD, class P>
+cudaError_t norm_go(const NormArgs& a, cudaStream_t st) {
+  constexpr int kResident = norm_resident(P::NI * P::V, BACKWARD);
+  const NormSplit s = norm_plan(a.D, a.H, (int64_t)a.B * a.L, sizeof(Act), P::LANES, kResident);
+  const unsigned grid = (unsigned)s.parts * (unsigned)s.heads_of_blocks;
+  if constexpr (!BACKWARD) {
+    constexpr auto kernel = norm_kernel<Act, GATE, P, kResident>;
+    const cudaError_t e = ensure_smem<kernel>(P::kBytes);
     if (e != cudaSuccess) return e;
-    const NormSplit s = norm_plan(a.D, a.H, tokens, sizeof(Act), F::LANES, kResident);
-    kernel<<<(unsigned)s.parts * (unsigned)s.heads_of_blocks, kNormThreads, F::kBytes, st>>>(a, s);
+    kernel<<<grid, kNormThreads, P::kBytes, st>>>(a, s);
     return cudaGetLastError();
+  } else {
+    constexpr auto kernel = norm_backward_kernel<Act, GATE, P, kResident>;
+    constexpr int kShared = norm_backward_shared<P>();
+    cudaError_t e = ensure_smem<kernel>(kShared);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kNormThreads, kShared, st>>>(a, s);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_norm_reduce(a, norm_partials(s, a.H, a.per_channel), st) : e;
   }
-  constexpr int kResident = norm_resident(B::NI * B::V, true);
-  constexpr auto kernel = norm_backward_kernel<Act, GATE, B, kResident>;
-  constexpr int kShared = norm_backward_shared<B>();
-  cudaError_t e = ensure_smem<kernel>(kShared);
-  if (e != cudaSuccess) return e;
-  const NormSplit s = norm_plan(a.D, a.H, tokens, sizeof(Act), B::LANES, kResident);
-  kernel<<<(unsigned)s.parts * (unsigned)s.heads_of_blocks, kNormThreads, kShared, st>>>(a, s);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_norm_reduce(a, norm_partials(s, a.H, a.per_channel), st) : e;
 }
 
-template <typename Act, bool GATE, int LANES, int NI>
-cudaError_t norm_ring(const NormArgs& a, bool backward, cudaStream_t st) {
-  constexpr int kF = GATE ? 2 : 1, kB = kF + 1;
-  return norm_go<Act, GATE, PiecesInShared<Act, LANES, NI, kF, NI <= 2 ? 4 : NI == 4 ? 3 : 2>,
-                 PiecesInShared<Act, LANES, NI, kB, NI == 1 ? 4 : NI == 2 ? 3 : 2>>(a, backward, st);
+// Rows of the ring by the bytes of each array that a lane holds of a row.
+constexpr int norm_stages(int bytes, bool backward) {
+  return bytes <= 4 ? 8 : bytes <= 8 ? 6 : bytes <= 16 ? 4 : bytes <= 32 ? (backward ? 3 : 4)
+                    : bytes <= 64 ? (backward ? 2 : 3) : 2;
 }
 
-template <typename Act, bool GATE, int LANES, int NI>
-cudaError_t norm_direct(const NormArgs& a, bool backward, cudaStream_t st) {
-  constexpr int kF = GATE ? 2 : 1;
-  return norm_go<Act, GATE, PiecesInRegisters<Act, LANES, NI, kF>,
-                 PiecesInRegisters<Act, LANES, NI, kF + 1>>(a, backward, st);
+// Pieces of V channels (V = 0: single ones that no asynchronous copy can take).
+template <typename Act, bool GATE, bool BACKWARD, int V, int LANES, int NI>
+cudaError_t norm_pieces(const NormArgs& a, cudaStream_t st) {
+  constexpr int N = (GATE ? 2 : 1) + (BACKWARD ? 1 : 0);
+  if constexpr (V == 0)
+    return norm_go<Act, GATE, BACKWARD, PiecesInRegisters<Act, LANES, NI, N>>(a, st);
+  else
+    return norm_go<Act, GATE, BACKWARD,
+                   PiecesInShared<Act, V, LANES, NI, N, norm_stages(NI * V * (int)sizeof(Act), BACKWARD)>>(a, st);
 }
 
-template <typename Act, int NI>
-cudaError_t norm_wide(const NormArgs& a, bool backward, cudaStream_t st) {
+template <typename Act, bool BACKWARD, int NI>
+cudaError_t norm_wide(const NormArgs& a, cudaStream_t st) {
   const int64_t tokens = (int64_t)a.B * a.L;
-  if (!backward) {
+  if constexpr (!BACKWARD) {
     norm_wide_kernel<Act, NI><<<(unsigned)std::min<int64_t>(tokens * a.H, kSms * 8), kNormThreads, 0, st>>>(a);
     return cudaGetLastError();
+  } else {
+    const int parts = norm_wide_parts(tokens, a.H);
+    norm_wide_backward_kernel<Act, NI><<<(unsigned)parts * (unsigned)a.H, kNormThreads, 0, st>>>(a, parts);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_norm_reduce(a, (int64_t)parts * a.H, st) : e;
   }
-  const int parts = norm_wide_parts(tokens, a.H);
-  norm_wide_backward_kernel<Act, NI><<<(unsigned)parts * (unsigned)a.H, kNormThreads, 0, st>>>(a, parts);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? launch_norm_reduce(a, (int64_t)parts * a.H, st) : e;
 }
 
-template <typename Act, bool GATE>
-cudaError_t norm_by_size(const NormArgs& a, bool backward, bool pieces, cudaStream_t st) {
-  if (a.D > kNormWide) {
-    if (a.D <= 2048) return norm_wide<Act, 8>(a, backward, st);
-    if (a.D <= 4096) return norm_wide<Act, 16>(a, backward, st);
-    return norm_wide<Act, 32>(a, backward, st);
-  }
-  constexpr int V = 16 / (int)sizeof(Act);
-  if (pieces) {
-    const int n = a.D / V;
-    switch (norm_lanes(n, 4)) {
-      case 4:
-        return norm_ring<Act, GATE, 4, 1>(a, backward, st);
-      case 8:
-        return norm_ring<Act, GATE, 8, 1>(a, backward, st);
-      case 16:
-        return norm_ring<Act, GATE, 16, 1>(a, backward, st);
-      default:
-        break;
-    }
-    if (n <= 32) return norm_ring<Act, GATE, 32, 1>(a, backward, st);
-    if (n <= 64) return norm_ring<Act, GATE, 32, 2>(a, backward, st);
-    if (n <= 128) return norm_ring<Act, GATE, 32, 4>(a, backward, st);
-    if constexpr (V == 4) return norm_ring<Act, GATE, 32, 8>(a, backward, st);
-  }
-  if (a.D <= 8) return norm_direct<Act, GATE, 8, 1>(a, backward, st);
-  if (a.D <= 32) return norm_direct<Act, GATE, 32, 1>(a, backward, st);
-  if (a.D <= 64) return norm_direct<Act, GATE, 32, 2>(a, backward, st);
-  if (a.D <= 128) return norm_direct<Act, GATE, 32, 4>(a, backward, st);
-  if (a.D <= 256) return norm_direct<Act, GATE, 32, 8>(a, backward, st);
-  if (a.D <= 512) return norm_direct<Act, GATE, 32, 16>(a, backward, st);
-  return norm_direct<Act, GATE, 32, 32>(a, backward, st);
+// Lanes and pieces per lane for rows of n pieces; cudaErrorNotSupported where a warp does not hold
+// them. A row costs a lane much the same however few channels it has there, so that a lane takes
+// 16 bytes of each array at the least (4 x 55 x 4096 rows of 36 channels backward, one piece of 8
+// bytes a lane: 2.2 TB/s).
+template <typename Act, bool GATE, bool BACKWARD, int V>
+cudaError_t norm_by_pieces(const NormArgs& a, int n, cudaStream_t st) {
+  constexpr int F = V == 0 ? 4 : 16 / (V * (int)sizeof(Act));
+  if (n <= 2 * F) return norm_pieces<Act, GATE, BACKWARD, V, 2, F>(a, st);
+  if (n <= 4 * F) return norm_pieces<Act, GATE, BACKWARD, V, 4, F>(a, st);
+  if (n <= 8 * F) return norm_pieces<Act, GATE, BACKWARD, V, 8, F>(a, st);
+  if (n <= 16 * F) return norm_pieces<Act, GATE, BACKWARD, V, 16, F>(a, st);
+  if (n <= 32 * F) return norm_pieces<Act, GATE, BACKWARD, V, 32, F>(a, st);
+  if (n <= 64 * F) return norm_pieces<Act, GATE, BACKWARD, V, 32, 2 * F>(a, st);
+  if (n <= 128 * F) return norm_pieces<Act, GATE, BACKWARD, V, 32, 4 * F>(a, st);
+  if constexpr (V * sizeof(Act) == 16 && sizeof(Act) == 4)
+    if (n <= 256) return norm_pieces<Act, GATE, BACKWARD, V, 32, 8>(a, st);
+  return cudaErrorNotSupported;
 }
 
-template <typename Act>
-cudaError_t launch_norm_as(const NormArgs& a, bool backward, cudaStream_t st) {
+// `wide`: channels that may be moved as one.
+template <typename Act, bool GATE, bool BACKWARD>
+cudaError_t norm_by_place(const NormArgs& a, int wide, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(Act);
-  const Tok* used[5] = {&a.x, &a.z, backward ? &a.grad_y : &a.y, backward ? &a.grad_x : &a.y,
-                        backward ? &a.grad_z : &a.y};
-  bool pieces = a.D % V == 0;
-  for (const Tok* t : used)
-    pieces = pieces && (t->p == nullptr ||
-                        (t->sb % V == 0 && t->sl % V == 0 && t->sh % V == 0 &&
-                         reinterpret_cast<uintptr_t>(t->p) % 16 == 0));
-  return a.z.p ? norm_by_size<Act, true>(a, backward, pieces, st)
-               : norm_by_size<Act, false>(a, backward, pieces, st);
+  cudaError_t e = cudaErrorNotSupported;
+  if (a.D <= kNormWarp) {
+    if (wide == V)
+      e = norm_by_pieces<Act, GATE, BACKWARD, V>(a, a.D / V, st);
+    else if (wide == V / 2)
+      e = norm_by_pieces<Act, GATE, BACKWARD, V / 2>(a, a.D / (V / 2), st);
+    else if (wide == V / 4)
+      e = norm_by_pieces<Act, GATE, BACKWARD, V / 4>(a, a.D / (V / 4), st);
+    else if constexpr (V == 8)  // single bf16 elements
+      e = norm_by_pieces<Act, GATE, BACKWARD, 0>(a, a.D, st);
+  }
+  if (e != cudaErrorNotSupported) return e;
+  if (a.D <= 1024) return norm_wide<Act, BACKWARD, 4>(a, st);
+  if (a.D <= 2048) return norm_wide<Act, BACKWARD, 8>(a, st);
+  if (a.D <= 4096) return norm_wide<Act, BACKWARD, 16>(a, st);
+  return norm_wide<Act, BACKWARD, 32>(a, st);
+}
+
+template <typename Act, bool BACKWARD>
+cudaError_t launch_norm_as(const NormArgs& a, cudaStream_t st) {
+  const Tok* used[5] = {&a.x, &a.z, BACKWARD ? &a.grad_y : &a.y, BACKWARD ? &a.grad_x : &a.y,
+                        BACKWARD ? &a.grad_z : &a.y};
+  int wide = 16 / (int)sizeof(Act);
+  for (bool fits = false; !fits && wide > 1; wide /= fits ? 1 : 2) {
+    fits = a.D % wide == 0;
+    for (const Tok* t : used)
+      fits = fits && (t->p == nullptr ||
+                      (t->sb % wide == 0 && t->sl % wide == 0 && t->sh % wide == 0 &&
+                       reinterpret_cast<uintptr_t>(t->p) % (wide * sizeof(Act)) == 0));
+  }
+  return a.z.p ? norm_by_place<Act, true, BACKWARD>(a, wide, st)
+               : norm_by_place<Act, false, BACKWARD>(a, wide, st);
 }
 
 }  // namespace gdnq

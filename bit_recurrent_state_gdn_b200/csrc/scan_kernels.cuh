@@ -239,10 +239,7 @@ struct RunsInShared {
         const int t = t0 + i + lane / kPieces;
         const bool ok = live && t >= 0 && t < len;
         const E* from = p + (ok ? (int64_t)t * sl : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                         to + (uint32_t)((i * kPieces + lane) * 16)),
-                     "l"(from), "r"(ok ? 16 : 0)
-                     : "memory");
+        async_piece<16>(to + (uint32_t)((i * kPieces + lane) * 16), from, ok);
       }
     }
   };

@@ -238,6 +238,19 @@ NORM = [
     (1, 3, 1, 8192, "bf16", True, True, False, "silu", "channel", "tokens", None),
     (60, 31, 8, 64, "bf16", False, False, True, "silu", "head", "heads", None),
     (3, 700, 6, 32, "f32", True, True, False, "silu", "channel", "tokens", [700, 1, 350]),
+    # pieces of 8 and 4 bytes, single elements, few lanes, more than a warp's
+    (2, 9, 5, 36, "bf16", True, True, True, "silu", "channel", "wide", None),
+    (2, 30, 3, 122, "bf16", False, True, True, "sigmoid", "channel", "heads", [30, 11]),
+    (1, 12, 3, 250, "bf16", True, False, True, "silu", "head", "tokens", None),
+    (1, 12, 3, 250, "f32", True, True, False, "silu", "channel", "heads", None),
+    (2, 50, 6, 7, "bf16", True, True, True, "silu", "channel", "tokens", [50, 20]),
+    (2, 50, 33, 8, "bf16", False, False, True, "silu", "head", "tokens", None),
+    (2, 20, 9, 2, "f32", True, True, False, "sigmoid", "channel", "heads", None),
+    (1, 9, 2, 333, "bf16", False, True, True, "silu", "head", "odd", None),
+    (1, 9, 2, 501, "f32", True, True, True, "silu", "channel", "odd", None),
+    (1, 7, 2, 600, "bf16", True, True, True, "silu", "head", "tokens", None),
+    (1, 7, 2, 999, "bf16", True, False, True, "none", "channel", "odd", [5]),
+    (1, 7, 1, 1024, "f32", False, True, True, "sigmoid", "head", "tokens", None),
 ]
 
 
