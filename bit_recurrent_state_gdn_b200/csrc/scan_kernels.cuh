@@ -7,7 +7,7 @@
 // first in the same way: with c the gradient that reaches a token's state from behind,
 // dh = grad_o + c, and c <- a dh, a run acts as c -> A c + R with the same A.
 //
-// Split. A warp takes 32 VEC channels and T consecutive tokens at a time in registers; W warps
+// Split. A warp takes 64 channels and T consecutive tokens at a time in registers; W warps
 // of a CTA (a group) and CL CTAs of a cluster take the runs that follow one another, join them
 // through shared memory, and walk the sequence together, the next tile's loads under way while
 // the present one is scanned. Each array is read and written once.
@@ -76,36 +76,50 @@ __device__ __forceinline__ F2 run_decay(F2 g_sum) {
   return a;
 }
 
-// VEC channels as they lie in memory; in registers a lane holds two, the second 0 for VEC = 1.
-template <typename T, int VEC>
-struct Raw;
-template <>
-struct Raw<float, 1> {
-  float v;
-  __device__ __forceinline__ F2 get() const { return f2(v, 0.0f); }
+// The channels of a slab, and a lane's two of them: neighbours (STEP = 1), which are moved as one,
+// or 32 apart (STEP = 32), one by one, where the arrays' alignment does not allow that.
+constexpr int kScanSlab = 64;
+
+struct ScanLane {
+  int c;             // the first one
+  bool live, both;   // whether it exists, and the second
+  int h, d, h2, d2;  // their places, or that of channel 0, or of the first
+};
+
+template <int STEP>
+__device__ __forceinline__ ScanLane scan_lane(const ScanArgs& a, int slab) {
+  const int lane = threadIdx.x & 31;
+  ScanLane l;
+  l.c = slab * kScanSlab + (STEP == 1 ? 2 * lane : lane);
+  l.live = l.c < a.C;
+  l.both = STEP == 1 ? l.live : l.c + STEP < a.C;
+  l.h = l.live ? l.c / a.D : 0;
+  l.d = l.live ? l.c % a.D : 0;
+  l.h2 = l.both ? (l.c + STEP) / a.D : l.h;
+  l.d2 = l.both ? (l.c + STEP) % a.D : l.d;
+  return l;
+}
+
+// The two channels as they lie in memory.
+template <typename T, int STEP>
+struct Raw {
+  T e[2];
+  __device__ __forceinline__ F2 get() const { return f2(Num<T>::to_f(e[0]), Num<T>::to_f(e[1])); }
   __device__ __forceinline__ void set(F2 f) {
-    float rest;
-    f2_get(f, v, rest);
+    float lo, hi;
+    f2_get(f, lo, hi);
+    e[0] = Num<T>::from_f(lo);
+    e[1] = Num<T>::from_f(hi);
   }
 };
 template <>
-struct Raw<float, 2> {
+struct Raw<float, 1> {
   float2 v;
   __device__ __forceinline__ F2 get() const { return f2(v.x, v.y); }
   __device__ __forceinline__ void set(F2 f) { f2_get(f, v.x, v.y); }
 };
 template <>
 struct Raw<__nv_bfloat16, 1> {
-  uint16_t v;
-  __device__ __forceinline__ F2 get() const { return f2(__uint_as_float((uint32_t)v << 16), 0.0f); }
-  __device__ __forceinline__ void set(F2 f) {
-    float lo, rest;
-    f2_get(f, lo, rest);
-    v = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-  }
-};
-template <>
-struct Raw<__nv_bfloat16, 2> {
   uint32_t v;
   __device__ __forceinline__ F2 get() const { return f2(bf16_lo(v), bf16_hi(v)); }
   __device__ __forceinline__ void set(F2 f) {
@@ -116,62 +130,104 @@ struct Raw<__nv_bfloat16, 2> {
   }
 };
 
-// A lane's column of a token array: VEC channels of every token. Rows are reached by 32-bit
+// A lane's column of a token array: its channels of every token. Rows are reached by 32-bit
 // offsets from the run's first one (the C entry points bound the stride). The stride passes
 // through an empty asm statement for every run: the compiler otherwise keeps the offsets of all T
 // rows of all arrays in registers through the loop over tiles, and spills.
-template <typename T, int VEC>
+__device__ __forceinline__ int opaque(int s) {
+  asm volatile("" : "+r"(s));
+  return s;
+}
+
+template <typename T, int STEP>
 struct Column {
-  T* p;
+  T *p, *q;  // the first channel; the second one, or the first where it does not exist
   int sl;
-  __device__ __forceinline__ Column(const Tok& t, int b, int h, int d)
-      : p(static_cast<T*>(t.p) + channel_offset(t, b, h, d)), sl((int)t.sl) {}
+  bool both;
+  __device__ __forceinline__ Column(const Tok& t, int b, const ScanLane& l)
+      : p(static_cast<T*>(t.p) + channel_offset(t, b, l.h, l.d)),
+        q(static_cast<T*>(t.p) + channel_offset(t, b, l.h2, l.d2)), sl((int)t.sl), both(l.both) {}
   struct Run {
-    T* p;
+    T *p, *q;
     int sl;
-    __device__ __forceinline__ Raw<T, VEC> load(int j) const {
-      return *reinterpret_cast<const Raw<T, VEC>*>(p + j * sl);
+    bool both;
+    __device__ __forceinline__ Raw<T, STEP> load(int j) const {
+      Raw<T, STEP> r;
+      r.e[0] = p[j * sl];
+      r.e[1] = q[j * sl];
+      return r;
     }
     __device__ __forceinline__ void store(int j, F2 f) const {
-      Raw<T, VEC> r;
+      Raw<T, STEP> r;
       r.set(f);
-      *reinterpret_cast<Raw<T, VEC>*>(p + j * sl) = r;
+      p[j * sl] = r.e[0];
+      if (both) q[j * sl] = r.e[1];
     }
   };
   __device__ __forceinline__ Run run(int t) const {
-    int s = sl;
-    asm volatile("" : "+r"(s));
+    const int s = opaque(sl);
+    return Run{p + (int64_t)t * s, q + (int64_t)t * s, s, both};
+  }
+};
+
+template <typename T>
+struct Column<T, 1> {
+  T* p;
+  int sl;
+  __device__ __forceinline__ Column(const Tok& t, int b, const ScanLane& l)
+      : p(static_cast<T*>(t.p) + channel_offset(t, b, l.h, l.d)), sl((int)t.sl) {}
+  struct Run {
+    T* p;
+    int sl;
+    __device__ __forceinline__ Raw<T, 1> load(int j) const {
+      return *reinterpret_cast<const Raw<T, 1>*>(p + j * sl);
+    }
+    __device__ __forceinline__ void store(int j, F2 f) const {
+      Raw<T, 1> r;
+      r.set(f);
+      *reinterpret_cast<Raw<T, 1>*>(p + j * sl) = r;
+    }
+  };
+  __device__ __forceinline__ Run run(int t) const {
+    const int s = opaque(sl);
     return Run{p + (int64_t)t * s, s};
   }
 };
+
+// The lane's two channels of an fp32 state that begins with its first one.
+template <int STEP>
+__device__ __forceinline__ F2 state_load(const float* p, bool both) {
+  return f2(p[0], STEP == 1 || both ? p[STEP] : 0.0f);
+}
+
+template <int STEP>
+__device__ __forceinline__ void state_store(float* p, bool both, F2 f) {
+  float lo, hi;
+  f2_get(f, lo, hi);
+  p[0] = lo;
+  if (STEP == 1 || both) p[STEP] = hi;
+}
 
 // The tokens of a warp's runs, tile after tile, as the scans read them: gate, input and (backward)
 // the gradient of the output. start() begins with the run at t0, `step` tokens from one tile to
 // the next; take() makes the next run readable; next() may begin the loads after it.
 //
 // RunsInRegisters: any alignment, one tile ahead in registers.
-template <typename Act, int VEC, int T, bool BACKWARD>
+template <typename Act, int STEP, int T, bool BACKWARD>
 struct RunsInRegisters {
-  static constexpr int kVec = VEC, kTokens = T;
+  static constexpr int kStep = STEP, kTokens = T;
   static constexpr int kBytes = 0;  // shared memory per warp
-  Column<float, VEC> gate;
-  Column<Act, VEC> in, grad;
+  Column<float, STEP> gate;
+  Column<Act, STEP> in, grad;
   bool live;
   int len, t0, step;
-  Raw<float, VEC> next_g[T];
-  Raw<Act, VEC> next_x[T], next_d[BACKWARD ? T : 1], now_x[T], now_d[BACKWARD ? T : 1];
+  Raw<float, STEP> next_g[T];
+  Raw<Act, STEP> next_x[T], next_d[BACKWARD ? T : 1], now_x[T], now_d[BACKWARD ? T : 1];
 
-  __device__ __forceinline__ RunsInRegisters(const ScanArgs& a, uint8_t*, int b, int c0, int len_)
-      : gate(a.g, b, 0, 0), in(a.x, b, 0, 0), grad(a.grad_o, b, 0, 0), len(len_) {
-    const int c = c0 + (threadIdx.x & 31) * VEC;
-    live = c < a.C;
-    if (live) {
-      const int h = c / a.D, d = c % a.D;
-      gate = Column<float, VEC>(a.g, b, h, d);
-      in = Column<Act, VEC>(a.x, b, h, d);
-      if constexpr (BACKWARD) grad = Column<Act, VEC>(a.grad_o, b, h, d);
-    }
-  }
+  __device__ __forceinline__ RunsInRegisters(const ScanArgs& a, uint8_t*, int b, int slab, int len_)
+      : gate(a.g, b, scan_lane<STEP>(a, slab)), in(a.x, b, scan_lane<STEP>(a, slab)),
+        grad(BACKWARD ? a.grad_o : a.x, b, scan_lane<STEP>(a, slab)),
+        live(scan_lane<STEP>(a, slab).live), len(len_) {}
   __device__ __forceinline__ void fetch() {
     const auto rg = gate.run(t0);
     const auto rx = in.run(t0), rd = grad.run(t0);
@@ -212,8 +268,8 @@ struct RunsInRegisters {
 // twice), so that neither the rows in flight nor their addresses take registers.
 template <typename Act, int T, int STAGES, bool BACKWARD>
 struct RunsInShared {
-  static constexpr int kVec = 2, kTokens = T;
-  static constexpr int kWide = 64;  // channels of a slab
+  static constexpr int kStep = 1, kTokens = T;
+  static constexpr int kWide = kScanSlab;
   static constexpr int kAct = T * kWide * (int)sizeof(Act);
   static constexpr int kStage = T * kWide * 4 + kAct * (BACKWARD ? 2 : 1);
   static constexpr int kBytes = STAGES * kStage;
@@ -250,9 +306,9 @@ struct RunsInShared {
   uint32_t ring;
   const uint8_t* now;
 
-  __device__ __forceinline__ RunsInShared(const ScanArgs& a, uint8_t* shared, int b, int c0, int len_)
-      : gate(a.g, a, b, c0), in(a.x, a, b, c0), grad(BACKWARD ? a.grad_o : a.x, a, b, c0), len(len_),
-        fill(0), read(0), ring(smem_u32(shared)), now(shared) {}
+  __device__ __forceinline__ RunsInShared(const ScanArgs& a, uint8_t* shared, int b, int slab, int len_)
+      : gate(a.g, a, b, slab * kWide), in(a.x, a, b, slab * kWide),
+        grad(BACKWARD ? a.grad_o : a.x, a, b, slab * kWide), len(len_), fill(0), read(0), ring(smem_u32(shared)), now(shared) {}
   __device__ __forceinline__ void fetch() {
     const uint32_t to = ring + (uint32_t)(fill * kStage);
     gate.copy(to, t0, len);
@@ -283,29 +339,15 @@ struct RunsInShared {
   }
   __device__ __forceinline__ void next() {}
   __device__ __forceinline__ F2 g(int j) const {
-    return reinterpret_cast<const Raw<float, 2>*>(now)[j * 32 + (threadIdx.x & 31)].get();
+    return reinterpret_cast<const Raw<float, 1>*>(now)[j * 32 + (threadIdx.x & 31)].get();
   }
   __device__ __forceinline__ F2 x(int j) const {
-    return reinterpret_cast<const Raw<Act, 2>*>(now + T * kWide * 4)[j * 32 + (threadIdx.x & 31)].get();
+    return reinterpret_cast<const Raw<Act, 1>*>(now + T * kWide * 4)[j * 32 + (threadIdx.x & 31)].get();
   }
   __device__ __forceinline__ F2 grad_o(int j) const {
-    return reinterpret_cast<const Raw<Act, 2>*>(now + T * kWide * 4 + kAct)[j * 32 + (threadIdx.x & 31)].get();
+    return reinterpret_cast<const Raw<Act, 1>*>(now + T * kWide * 4 + kAct)[j * 32 + (threadIdx.x & 31)].get();
   }
 };
-
-// Two channels of an fp32 state, the second one only for VEC = 2.
-template <int VEC>
-__device__ __forceinline__ F2 state_load(const float* p) {
-  return f2(p[0], VEC == 2 ? p[VEC - 1] : 0.0f);
-}
-
-template <int VEC>
-__device__ __forceinline__ void state_store(float* p, F2 f) {
-  float lo, hi;
-  f2_get(f, lo, hi);
-  p[0] = lo;
-  if (VEC == 2) p[VEC - 1] = hi;
-}
 
 // One lane's share of what runs hand each other.
 struct Link {
@@ -330,7 +372,7 @@ constexpr int scan_threads(int W) { return 32 * W * scan_groups(W); }
 
 template <typename Act, int SCALE, class Runs, int W, int CL, int MINB>
 __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a, int slabs) {
-  constexpr int kGroups = scan_groups(W), VEC = Runs::kVec, T = Runs::kTokens;
+  constexpr int kGroups = scan_groups(W), STEP = Runs::kStep, T = Runs::kTokens;
   extern __shared__ __align__(128) uint8_t rings[];
   static_assert(GDN_SCAN_CHUNK % T == 0, "kept states stand where runs begin");
   __shared__ alignas(16) Link agg[W > 1 ? 2 : 1][W][W > 1 ? 32 : 1];
@@ -340,17 +382,17 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
   const int64_t unit = CL > 1 ? blockIdx.x / CL
                               : (int64_t)blockIdx.x * kGroups + (W > 1 ? 0 : threadIdx.x >> 5);
   if (W == 1 && unit >= (int64_t)a.B * slabs) return;  // no barrier waits for this warp
-  const int b = (int)(unit / slabs), c = (int)(unit % slabs) * 32 * VEC + lane * VEC;
-  const bool live = c < a.C;
-  const int hd = live ? c / a.D : 0, d = live ? c % a.D : 0;
+  const int b = (int)(unit / slabs), slab = (int)(unit % slabs);
+  const ScanLane me = scan_lane<STEP>(a, slab);
+  const bool live = me.live;
   const int len = seq_len(a.lens, b, a.L);
-  const Column<Act, VEC> o(a.o, b, hd, d);
-  Runs runs(a, rings + (threadIdx.x >> 5) * Runs::kBytes, b, (int)(unit % slabs) * 32 * VEC, len);
-  const int64_t state = (int64_t)b * a.C + c;
+  const Column<Act, STEP> o(a.o, b, me);
+  Runs runs(a, rings + (threadIdx.x >> 5) * Runs::kBytes, b, slab, len);
+  const int64_t state = (int64_t)b * a.C + me.c;
   float* hist = a.hist && live
-                    ? a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + c
+                    ? a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + me.c
                     : nullptr;
-  F2 carry = a.h0 && live ? state_load<VEC>(a.h0 + state) : f2_all(0.0f);  // before the tile
+  F2 carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);  // before the tile
 
   constexpr int kTile = CL * W * T;
   int t0 = (rank * W + w) * T;
@@ -404,7 +446,7 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
       }
     }
     if (hist && t0 % GDN_SCAN_CHUNK == 0 && t0 < len)
-      state_store<VEC>(hist + (int64_t)(t0 / GDN_SCAN_CHUNK) * a.C, h);
+      state_store<STEP>(hist + (int64_t)(t0 / GDN_SCAN_CHUNK) * a.C, me.both, h);
     const auto ro = o.run(t0);
     if (live && t0 + T <= len) {
 #pragma unroll
@@ -421,7 +463,7 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
     }
     if constexpr (W == 1) carry = h;
   }
-  if (a.hT && live && rank == 0 && w == 0) state_store<VEC>(a.hT + state, carry);
+  if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);
 }
 
 // A CTA's tile is one chunk between kept states.
@@ -429,7 +471,7 @@ template <typename Act, int SCALE, class Runs, int CL, int MINB>
 __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
     scan_backward_kernel(ScanArgs a, int slabs) {
   constexpr int T = Runs::kTokens, W = GDN_SCAN_CHUNK / T;
-  constexpr int VEC = Runs::kVec;
+  constexpr int STEP = Runs::kStep;
   extern __shared__ __align__(128) uint8_t rings[];
   __shared__ alignas(16) Link agg[2][W][32];  // decay and forward scan of each run
   __shared__ F2 agg_back[2][W][32];           // its scan of the gradient
@@ -437,23 +479,23 @@ __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
   const int64_t unit = blockIdx.x / CL;
-  const int b = (int)(unit / slabs), c = (int)(unit % slabs) * 32 * VEC + lane * VEC;
-  const bool live = c < a.C;
-  const int hd = live ? c / a.D : 0, d = live ? c % a.D : 0;
+  const int b = (int)(unit / slabs), slab = (int)(unit % slabs);
+  const ScanLane me = scan_lane<STEP>(a, slab);
+  const bool live = me.live;
   const int len = seq_len(a.lens, b, a.L);
-  const Column<Act, VEC> gx(a.grad_x, b, hd, d);
-  const Column<float, VEC> gg(a.grad_g, b, hd, d);
-  Runs runs(a, rings + w * Runs::kBytes, b, (int)(unit % slabs) * 32 * VEC, len);
-  const int64_t state = (int64_t)b * a.C + c;
+  const Column<Act, STEP> gx(a.grad_x, b, me);
+  const Column<float, STEP> gg(a.grad_g, b, me);
+  Runs runs(a, rings + w * Runs::kBytes, b, slab, len);
+  const int64_t state = (int64_t)b * a.C + me.c;
   const float* hist =
-      a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + c;
+      a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + me.c;
   // the gradient that reaches the tile's last state from behind
-  F2 carry = a.h0 && live ? state_load<VEC>(a.h0 + state) : f2_all(0.0f);
+  F2 carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);
 
   // the kept state before the CTA's tile that begins at `first`
   auto kept = [&](int first) {
     return live && first >= 0 && first < len
-               ? state_load<VEC>(hist + (int64_t)(first / GDN_SCAN_CHUNK) * a.C)
+               ? state_load<STEP>(hist + (int64_t)(first / GDN_SCAN_CHUNK) * a.C, me.both)
                : f2_all(0.0f);
   };
 
@@ -520,11 +562,16 @@ __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
         carry = f2_fma(agg[buf][i][lane].a, carry, agg_back[buf][i][lane]);
       }
     }
-    F2 before[T];
+    F2 before[T];  // the state before each token, and what the slope of s adds to it
 #pragma unroll
     for (int j = 0; j < T; ++j) {
+      const F2 xj = runs.x(j);
+      // with s' = -a for 1 - a and -a^2 / s for sqrt(1 - a^2), grad_g = a dh (h + s' x / a)
       before[j] = h;
-      h = f2_fma(at[j], h, f2_mul(s[j], runs.x(j)));
+      if constexpr (SCALE == GDN_SCALE_COMPLEMENT) before[j] = f2_fma(xj, f2_all(-1.0f), h);
+      if constexpr (SCALE == GDN_SCALE_SQRT)
+        before[j] = f2_fma(f2_mul(f2_mul(at[j], f2_all(-1.0f)), r[j]), xj, h);
+      h = f2_fma(at[j], h, f2_mul(s[j], xj));
     }
     const auto wx = gx.run(t0);
     const auto wg = gg.run(t0);
@@ -534,18 +581,13 @@ __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
       const F2 dh = f2_add(runs.grad_o(j), dc);
       const F2 dx = f2_mul(s[j], dh);
       dc = f2_mul(at[j], dh);
-      // a h dh + s' x dh, with s' = -a for 1 - a and -a^2 / s for sqrt(1 - a^2)
-      F2 k = before[j];
-      if constexpr (SCALE == GDN_SCALE_COMPLEMENT) k = f2_fma(runs.x(j), f2_all(-1.0f), k);
-      if constexpr (SCALE == GDN_SCALE_SQRT)
-        k = f2_fma(f2_mul(f2_mul(at[j], f2_all(-1.0f)), r[j]), runs.x(j), k);
       if (whole || (live && t0 + j < len)) {
         wx.store(j, dx);
-        wg.store(j, f2_mul(dc, k));
+        wg.store(j, f2_mul(dc, before[j]));
       }
     }
   }
-  if (a.hT && live && rank == 0 && w == 0) state_store<VEC>(a.hT + state, carry);
+  if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);
 }
 
 }  // namespace gdnq

@@ -46,7 +46,7 @@ cudaError_t scan_back(const ScanArgs& a, int slabs, cudaStream_t st) {
   return launch_in_clusters(kernel, (int64_t)a.B * slabs * CL, 32 * W, CL, kShared, st, a, slabs);
 }
 
-// CTAs that share a unit (the 32 kVec channels of one sequence) as a cluster: where units are
+// CTAs that share a unit (a slab of channels of one sequence) as a cluster: where units are
 // few, as many as two CTAs per SM hold, each with a tile of its own to take.
 inline int scan_cluster(int64_t units, int tile, int L) {
   int cl = 1;
@@ -71,19 +71,18 @@ inline ScanSplit scan_split(int64_t units, int L, int run) {
 
 template <typename Act, int SCALE, class P>
 cudaError_t launch_scan_plan(const ScanArgs& a, bool backward, cudaStream_t st) {
-  constexpr int kWide = 32 * P::Back::kVec;
-  const int slabs = (a.C + kWide - 1) / kWide;
+  const int slabs = (a.C + kScanSlab - 1) / kScanSlab;
   const int64_t units = (int64_t)a.B * slabs;
   if (backward) {
     switch (scan_cluster(units, GDN_SCAN_CHUNK, a.L)) {
       case 1:
-        return scan_back<Act, SCALE, typename P::Back, 1, 2>(a, slabs, st);
+        return scan_back<Act, SCALE, typename P::Back, 1, P::kBackResident>(a, slabs, st);
       case 2:
-        return scan_back<Act, SCALE, typename P::Back, 2, 2>(a, slabs, st);
+        return scan_back<Act, SCALE, typename P::Back, 2, P::kBackResident>(a, slabs, st);
       case 4:
-        return scan_back<Act, SCALE, typename P::Back, 4, 2>(a, slabs, st);
+        return scan_back<Act, SCALE, typename P::Back, 4, P::kBackResident>(a, slabs, st);
       default:
-        return scan_back<Act, SCALE, typename P::Back, 8, 2>(a, slabs, st);
+        return scan_back<Act, SCALE, typename P::Back, 8, P::kBackResident>(a, slabs, st);
     }
   }
   if (a.L <= 1) return scan_forward<Act, SCALE, typename P::One, 1, 1, 4>(a, slabs, st);
@@ -112,21 +111,23 @@ cudaError_t launch_scan_plan(const ScanArgs& a, bool backward, cudaStream_t st) 
 template <typename Act>
 struct PlanShared {
   static constexpr bool kF32 = sizeof(Act) == 4;
-  using One = RunsInRegisters<Act, 2, 1, false>;
+  using One = RunsInRegisters<Act, 1, 1, false>;
   using Alone = RunsInShared<Act, 8, 4, false>;
   using Four = RunsInShared<Act, 16, 2, false>;
   using Eight = RunsInShared<Act, kF32 ? 8 : 16, kF32 ? 3 : 2, false>;
   using Back = RunsInShared<Act, 16, 2, true>;
+  static constexpr int kBackResident = 2;
 };
 
-// Any other placement: VEC channels at a time.
-template <typename Act, int VEC>
+// Any other placement: neighbouring channels (STEP = 1), or one by one (32).
+template <typename Act, int STEP>
 struct PlanRegisters {
-  using One = RunsInRegisters<Act, VEC, 1, false>;
-  using Alone = RunsInRegisters<Act, VEC, 8, false>;
+  using One = RunsInRegisters<Act, STEP, 1, false>;
+  using Alone = RunsInRegisters<Act, STEP, 8, false>;
   using Four = Alone;
   using Eight = Alone;
-  using Back = RunsInRegisters<Act, VEC, 8, true>;
+  using Back = RunsInRegisters<Act, STEP, 8, true>;
+  static constexpr int kBackResident = 1;  // two spill (3875 channels, 8 x 1000 tokens: 1.5 / 2.2 TB/s)
 };
 
 // Whether `n` channels may be moved as one in every array: they lie in one head and are aligned.
@@ -161,8 +162,8 @@ cudaError_t launch_scan_scale(ScanArgs a, bool backward, cudaStream_t st) {
   for (const Used& u : written) pairs = pairs && aligned(*u.t, a.D, 2, u.elem);
   // 16-byte pieces, channel pairs, single channels
   if (pairs && pieces) return launch_scan_plan<Act, SCALE, PlanShared<Act>>(a, backward, st);
-  if (pairs) return launch_scan_plan<Act, SCALE, PlanRegisters<Act, 2>>(a, backward, st);
-  return launch_scan_plan<Act, SCALE, PlanRegisters<Act, 1>>(a, backward, st);
+  if (pairs) return launch_scan_plan<Act, SCALE, PlanRegisters<Act, 1>>(a, backward, st);
+  return launch_scan_plan<Act, SCALE, PlanRegisters<Act, 32>>(a, backward, st);
 }
 
 template <typename Act>
