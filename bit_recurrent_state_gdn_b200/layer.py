@@ -129,7 +129,9 @@ class _Args:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
         if need >= 0:
             if workspace is None and need > 0:
-                on = torch.cuda.ExternalStream(handle) if stream is not None else None
+                on = None  # the current stream, which torch allocates for
+                if stream is not None:
+                    on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
                 with torch.cuda.stream(on):
                     workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
             if workspace is None:

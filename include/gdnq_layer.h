@@ -19,7 +19,8 @@
  *   - Activations (GDN_DTYPE_BF16 or GDN_DTYPE_F32) are rounded once, to nearest even, when they
  *     are stored; parameters, their gradients, log-gates and scan states are fp32, and all
  *     arithmetic is fp32. Results do not depend on the order in which CTAs run.
- *   - Sizes: L <= 2^30, H D <= 2^30, B H < 2^31, B H D <= 2^36; offsets inside arrays are 64-bit.
+ *   - Sizes: L <= 2^30, H D <= 2^30, B H < 2^31, B H D <= 2^36; offsets inside arrays are 64-bit,
+ *     tokens at most 2^27 elements apart (GDN_ERR_UNSUPPORTED beyond).
  *   - Errors: GDN_ERR_INVALID_ARG for a null or misaligned pointer, a bad size, stride or enum
  *     value, or a workspace too small; GDN_ERR_UNSUPPORTED for a size that is not built;
  *     GDN_ERR_CUDA for a failed launch.
@@ -63,7 +64,9 @@ typedef struct {
  * number (the matrix state of gdnq.h without keys and queries):
  *     h_t = a_t h_{t-1} + s(g_t) x_t,   a_t = e^{g_t},   o_t = h_t.
  * g_t = -inf forgets all before (the first token of a document in a packed row); g_t = 0 with
- * x_t = 0 changes nothing.
+ * x_t = 0 changes nothing. Runs of tokens are joined by the exponential of their summed gates: a
+ * gate above 1 (g_t > 0, not with GDN_SCALE_SQRT) is taken too, as long as no 1024 tokens' gates
+ * sum to 88 or more. Gates below 2^-126 count as zero.
  *   x     act tokens;  g  fp32 tokens, the log of the gate;  o  act tokens, written.
  *   h0    fp32 [B][H][D], the states before the first token, or NULL: zero.
  *   hT    fp32 [B][H][D], the states after each sequence's last token, or NULL; may be h0.

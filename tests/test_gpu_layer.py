@@ -552,6 +552,57 @@ def test_conv_gradients_against_differences():
         difference(f, [x, w, b, s], [dx, dw, db, ds], i, 51 + i)
 
 
+@pytest.mark.parametrize("dims,strides", [
+    ((2, 20, 2, 64), (2 ** 31 + 64, 128, 64)),      # sequences further apart than 2^31 elements
+    ((1, 20, 2, 64), (0, 2 ** 27, 64)),             # tokens as far apart as they may be
+])
+def test_arrays_far_apart(dims, strides):
+    """Offsets beyond 32 bits, read and written, in all three operators."""
+    B, L, H, D = dims
+    n = sum((d - 1) * s for d, s in zip(dims, strides)) + D
+    free = torch.cuda.mem_get_info()[0]
+    if free < 4 * n + (2 << 30):
+        pytest.skip("needs two arrays of that size")
+
+    def far(t):
+        out = torch.empty(n, dtype=torch.bfloat16, device="cuda").as_strided(dims, (*strides, 1))
+        return out.copy_(t)
+
+    x, g, h0, _ = scan_inputs(B, L, H, D, "bf16", None, seed=80)
+    xs, out = far(x), far(torch.full_like(x, MARK))
+    gdn.gdn_gated_scan(gdn.make_scan_config(B, H, D), xs, g.cuda(), out, h0=h0.cuda())
+    want, _, _, err, _, _ = ref.scan(x, g, h0, "none")
+    close(out, want, err, torch.bfloat16, "scan")
+    w = torch.ones(D)
+    gdn.gdn_group_norm(gdn.make_norm_config(B, H, D), xs, w.cuda(), out)
+    close(out, *ref.norm(x, w, None, None, "none", False, 1e-6), torch.bfloat16, "norm")
+    w = torch.randn((H * D, 4), generator=gen(81))
+    gdn.gdn_short_conv(gdn.make_conv_config(B, H, D, 4), xs, w.cuda(), out)
+    want, _, err = ref.conv(x.view(B, L, -1), w, None, torch.zeros((B, 3, H * D)), "silu")
+    close(out, want.view(x.shape), err.view(x.shape), torch.bfloat16, "conv")
+
+
+def test_two_layers_at_once():
+    """The same layer on two streams side by side, each with arrays and workspaces of its own."""
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    sets = [layer_state(90 + i, B=3, L=700, H=4) for i in range(2)]
+    want = []
+    for t, bufs in sets:
+        run_layer(t, bufs)
+        torch.cuda.synchronize()
+        want.append({n: v.clone() for n, v in bufs.items()})
+        for v in bufs.values():
+            v.fill_(MARK)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for side, (t, bufs) in zip(sides, sets):
+            run_layer(t, bufs, stream=side)
+    torch.cuda.synchronize()
+    for (t, bufs), w in zip(sets, want):
+        for n in w:
+            assert torch.equal(bufs[n], w[n]), n
+
+
 def layer(x, w_conv, g, w_norm, z, h0, bufs, stream=None):
     """conv -> scan -> gated norm, as a layer calls them."""
     B, L, H, D = x.shape

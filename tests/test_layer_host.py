@@ -77,6 +77,7 @@ def test_bad_token_arrays_are_refused(lib, op):
     assert call(lib, f32, x=tok(4098)) == BAD
     assert call(lib, cfg, x=tok(sl=-64)) == BAD
     assert call(lib, cfg, x=tok(sb=1 << 62)) == BAD            # offsets overflow
+    assert call(lib, cfg, x=tok(sb=1 << 40, sl=(1 << 27) + 1)) == LACK
     assert call(lib, cfg, **{out: tok(12288, sl=0)}) == BAD    # written elements share memory
     assert call(lib, cfg, **{out: tok(12288, sh=15)}) == BAD
     assert call(lib, cfg, **{out: tok(12288, sl=63)}) == BAD
