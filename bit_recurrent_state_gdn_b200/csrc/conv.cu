@@ -11,6 +11,7 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(ConvArgs a, int parts)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = (int64_t)a.C * (a.K + 1), i = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
+  wait_for_last();
   if (i < n)
     for (int p = warp; p < parts; p += 8) s += a.partials[p * n + i];
   sum[warp][lane] = s;
@@ -30,8 +31,7 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(ConvArgs a, int parts)
 
 cudaError_t launch_conv_reduce(const ConvArgs& a, int parts, cudaStream_t st) {
   const int64_t n = (int64_t)a.C * (a.K + 1);
-  conv_reduce_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(a, parts);
-  return cudaGetLastError();
+  return launch_behind(conv_reduce_kernel, (unsigned)((n + 31) / 32), 256, st, a, parts);
 }
 
 // Large enough for any placement of the arrays, on which the split depends.

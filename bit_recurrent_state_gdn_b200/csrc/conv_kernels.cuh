@@ -370,6 +370,7 @@ template <typename Act, int K, bool SILU, class Rows, int TX, int MINB>
 __global__ void __launch_bounds__(kConvThreads, MINB) conv_backward_kernel(ConvArgs a, ConvSplit split) {
   constexpr int V = Rows::V, P = Vec<Act, V>::P, TY = kConvThreads / TX;
   extern __shared__ __align__(128) uint8_t rings[];
+  let_next_launch();
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   const int slabs = (split.columns + TX - 1) / TX;
   const int slab = (int)(blockIdx.x % (unsigned)slabs), part = (int)(blockIdx.x / (unsigned)slabs);
@@ -385,7 +386,9 @@ __global__ void __launch_bounds__(kConvThreads, MINB) conv_backward_kernel(ConvA
   if (column < split.columns) {
     const int hd = c / a.D, d = c % a.D;
     taps<V, K>(a, c, w, bias);
-    for (int64_t r = (int64_t)part * TY + ty; r < (int64_t)a.B * split.runs;
+    // a CTA's runs lie far apart: in a padded batch every CTA has its share of the runs behind the
+    // sequences' ends (4 sequences, 88 % of the tokens: 92 us with neighbouring runs)
+    for (int64_t r = (int64_t)ty * split.parts + part; r < (int64_t)a.B * split.runs;
          r += (int64_t)split.parts * TY) {
       const int b = (int)(r / split.runs), t0 = (int)(r % split.runs) * split.run_tokens;
       const int len = seq_len(a.lens, b, a.L), t1 = min(t0 + split.run_tokens, len);

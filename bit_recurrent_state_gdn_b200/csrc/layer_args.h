@@ -65,6 +65,23 @@ inline int64_t shares(int64_t slots, int64_t units) {
   return fit >= 4 ? fit : (4 * slots + units - 1) / units;
 }
 
+// Launches the kernel that adds partial sums behind the one that forms them, so that its launch
+// overlaps that one's end (the kernels say let_next_launch and wait_for_last).
+template <typename... Params>
+cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, int threads, cudaStream_t st,
+                          Params... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Forward or backward scan, by activation type; scale is a gdn_input_scale.
 cudaError_t launch_scan_f32(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
 cudaError_t launch_scan_bf16(const ScanArgs& a, int scale, bool backward, cudaStream_t st);

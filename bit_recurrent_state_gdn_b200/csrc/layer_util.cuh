@@ -42,6 +42,11 @@ __device__ __forceinline__ void async_piece(uint32_t to, const void* from) {
                  : "memory");
 }
 
+// A kernel whose partial sums a second one adds lets that one be launched while it still runs; the
+// second waits for all of the first one's work before it reads.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 // 1 / sqrt(x) on the hardware path.
 __device__ __forceinline__ float rsqrt_hw(float x) {
   float y;

@@ -12,6 +12,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(NormArgs a, int64_t c
   const int64_t n = a.per_channel ? (int64_t)a.H * a.D : a.D;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float2 s = make_float2(0.0f, 0.0f);
+  wait_for_last();
   if (c < n) {
     const int64_t step = a.per_channel ? a.H : 1;
     const float* p = a.partials + c / a.D * 2 * a.D + c % a.D;
@@ -36,8 +37,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(NormArgs a, int64_t c
 
 cudaError_t launch_norm_reduce(const NormArgs& a, int64_t partials, cudaStream_t st) {
   const int64_t n = a.per_channel ? (int64_t)a.H * a.D : a.D;
-  norm_reduce_kernel<<<(unsigned)((n + 31) / 32), 1024, 0, st>>>(a, partials);
-  return cudaGetLastError();
+  return launch_behind(norm_reduce_kernel, (unsigned)((n + 31) / 32), 1024, st, a, partials);
 }
 
 // Large enough for any placement of the arrays, on which the split of the rows depends.

@@ -323,17 +323,19 @@ __global__ void __launch_bounds__(kNormThreads, MINB) norm_kernel(NormArgs a, No
     if constexpr (GATE) Lane::get(pieces, 1, z);
     pieces.done();
     fetch();
-    q.normalise(a, x);
-    with_activation(a.activation, [&](auto act) {
+    if (__any_sync(~0u, live)) {  // not behind the ends of all of the warp's sequences
+      q.normalise(a, x);
+      with_activation(a.activation, [&](auto act) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const F2 u = f2_fma(x[e], w[e], bias[e]);
-        F2 v, slope;
-        act_pair<decltype(act)::value, false>(GATE ? z[e] : u, v, slope);
-        x[e] = GATE ? f2_mul(u, v) : v;
-      }
-    });
-    q.put(y_at.p, live, x);
+        for (int e = 0; e < E; ++e) {
+          const F2 u = f2_fma(x[e], w[e], bias[e]);
+          F2 v, slope;
+          act_pair<decltype(act)::value, false>(GATE ? z[e] : u, v, slope);
+          x[e] = GATE ? f2_mul(u, v) : v;
+        }
+      });
+      q.put(y_at.p, live, x);
+    }
     at.next(a.L);
     y_at.next(at);
   }
@@ -353,6 +355,7 @@ __global__ void __launch_bounds__(kNormThreads, MINB) norm_backward_kernel(NormA
   using Lane = NormLane<P>;
   constexpr int N = GATE ? 3 : 2, NI = P::NI, V = P::V, E = Lane::E, LANES = P::LANES;
   extern __shared__ __align__(128) uint8_t rings[];
+  let_next_launch();
   const Lane q(a, split);
   F2 w[E], bias[E], sw[E], sb[E];
   q.weights(a, a.w, w);
@@ -392,31 +395,33 @@ __global__ void __launch_bounds__(kNormThreads, MINB) norm_backward_kernel(NormA
     if constexpr (GATE) Lane::get(pieces, 2, z);
     pieces.done();
     fetch();
-    const float rstd = q.normalise(a, x);
-    F2 s1 = f2_all(0.0f), s2 = s1;
-    with_activation(a.activation, [&](auto act) {
+    if (__any_sync(~0u, live)) {  // not behind the ends of all of the warp's sequences
+      const float rstd = q.normalise(a, x);
+      F2 s1 = f2_all(0.0f), s2 = s1;
+      with_activation(a.activation, [&](auto act) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const F2 u = f2_fma(x[e], w[e], bias[e]);
-        F2 v, slope;
-        act_pair<decltype(act)::value, true>(GATE ? z[e] : u, v, slope);
-        const F2 du = f2_mul(dy[e], GATE ? v : slope);
-        if constexpr (GATE) z[e] = f2_mul(f2_mul(dy[e], u), slope);  // grad_z
-        sw[e] = f2_fma(du, x[e], sw[e]);
-        sb[e] = f2_add(sb[e], du);
-        dy[e] = f2_mul(du, w[e]);  // dn
-        s1 = f2_add(s1, dy[e]);
-        s2 = f2_fma(dy[e], x[e], s2);
-      }
-    });
-    const float m1 = a.center ? lanes_sum<LANES>(f2_sum(s1)) * a.inv_d : 0.0f;
-    const float m2 = lanes_sum<LANES>(f2_sum(s2)) * a.inv_d;
-    // rstd (dn - m1 - n m2)
+        for (int e = 0; e < E; ++e) {
+          const F2 u = f2_fma(x[e], w[e], bias[e]);
+          F2 v, slope;
+          act_pair<decltype(act)::value, true>(GATE ? z[e] : u, v, slope);
+          const F2 du = f2_mul(dy[e], GATE ? v : slope);
+          if constexpr (GATE) z[e] = f2_mul(f2_mul(dy[e], u), slope);  // grad_z
+          sw[e] = f2_fma(du, x[e], sw[e]);
+          sb[e] = f2_add(sb[e], du);
+          dy[e] = f2_mul(du, w[e]);  // dn
+          s1 = f2_add(s1, dy[e]);
+          s2 = f2_fma(dy[e], x[e], s2);
+        }
+      });
+      const float m1 = a.center ? lanes_sum<LANES>(f2_sum(s1)) * a.inv_d : 0.0f;
+      const float m2 = lanes_sum<LANES>(f2_sum(s2)) * a.inv_d;
+      // rstd (dn - m1 - n m2)
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      dy[e] = f2_fma(dy[e], f2_all(rstd), f2_mul(f2_fma(x[e], f2_all(m2), f2_all(m1)), f2_all(-rstd)));
-    q.put(dx_at.p, live, dy);
-    if constexpr (GATE) q.put(dz_at.p, live, z);
+      for (int e = 0; e < E; ++e)
+        dy[e] = f2_fma(dy[e], f2_all(rstd), f2_mul(f2_fma(x[e], f2_all(m2), f2_all(m1)), f2_all(-rstd)));
+      q.put(dx_at.p, live, dy);
+      if constexpr (GATE) q.put(dz_at.p, live, z);
+    }
     at.next(a.L);
     dx_at.next(at);
     if constexpr (GATE) dz_at.next(at);
@@ -534,6 +539,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(NormArgs a) {
 // CTA = (part, head): every parts-th token of its head.
 template <typename Act, int NI>
 __global__ void __launch_bounds__(kNormThreads) norm_wide_backward_kernel(NormArgs a, int parts) {
+  let_next_launch();
   const int h = (int)(blockIdx.x % (unsigned)a.H), part = (int)(blockIdx.x / (unsigned)a.H);
   const int64_t base = a.per_channel ? (int64_t)h * a.D : 0;
   float w[NI], bias[NI], sw[NI], sb[NI];
