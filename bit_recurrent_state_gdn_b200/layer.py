@@ -115,34 +115,31 @@ class _Args:
     def lens(self, t):
         return None if t is None else self.dense(t, "lens", torch.int32, self.shape[0])
 
-    def call(self, where: str, args, stream, workspace=None, need: int = -1):
-        """The C entry point ``where`` on args, the workspace of ``need`` bytes (calls that have
-        one) and the stream, with the tensors' device current."""
+    def call(self, where: str, cfg, args, stream, workspace=None, need=None):
+        """The C entry point ``where`` on cfg, L and args, the workspace (of ``need(cfg, L)`` bytes,
+        in calls that have one) and the stream, with the tensors' device current."""
         if self.index < 0:
             raise ValueError(f"{where}: the tensors are on {self.device}, expected a CUDA device")
         if self.index != torch.cuda.current_device():
             with torch.cuda.device(self.index):
-                return self.call(where, args, stream, workspace, need)
+                return self.call(where, cfg, args, stream, workspace, need)
         if stream is None:
             handle = _current_stream(self.index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
-        if need >= 0:
-            if workspace is None and need > 0:
+        if need is not None:
+            if workspace is None:
+                n = need(cfg, self.shape[1])
                 on = None  # the current stream, which torch allocates for
                 if stream is not None:
                     on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
                 with torch.cuda.stream(on):
-                    workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
-            if workspace is None:
-                args += (None, 0)
-            else:
-                self.on_device(workspace, "workspace")
-                if not workspace.is_contiguous():
-                    raise ValueError("workspace must be contiguous")
-                args += (workspace.data_ptr() or None,
-                         workspace.numel() * workspace.element_size())
-        status = getattr(_abi.load(), where)(*args, handle)
+                    workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+            self.on_device(workspace, "workspace")
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+            args += (workspace.data_ptr() or None, workspace.numel() * workspace.element_size())
+        status = getattr(_abi.load(), where)(byref(cfg), self.shape[1], *args, handle)
         if status:
             raise GdnError(status, where)
 
@@ -153,8 +150,8 @@ def gdn_gated_scan(cfg, x, g, o, h0=None, hT=None, hist=None, lens=None, stream=
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
     n = cfg.B * cfg.H * cfg.D
     f32, L = torch.float32, a.shape[1]
-    a.call("gdn_gated_scan", (
-        byref(cfg), L, a.tokens(x, "x", act), a.tokens(g, "g", f32), a.tokens(o, "o", act),
+    a.call("gdn_gated_scan", cfg, (
+        a.tokens(x, "x", act), a.tokens(g, "g", f32), a.tokens(o, "o", act),
         a.dense(h0, "h0", f32, n), a.dense(hT, "hT", f32, n),
         a.dense(hist, "hist", f32, n * -(-L // _abi.GDN_SCAN_CHUNK)), a.lens(lens)), stream)
 
@@ -166,8 +163,8 @@ def gdn_gated_scan_backward(cfg, x, g, hist, do, dx, dg, dhT=None, dh0=None, len
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
     n = cfg.B * cfg.H * cfg.D
     f32, L = torch.float32, a.shape[1]
-    a.call("gdn_gated_scan_backward", (
-        byref(cfg), L, a.tokens(x, "x", act), a.tokens(g, "g", f32),
+    a.call("gdn_gated_scan_backward", cfg, (
+        a.tokens(x, "x", act), a.tokens(g, "g", f32),
         a.dense(hist, "hist", f32, n * -(-L // _abi.GDN_SCAN_CHUNK)), a.tokens(do, "do", act),
         a.dense(dhT, "dhT", f32, n), a.tokens(dx, "dx", act), a.tokens(dg, "dg", f32),
         a.dense(dh0, "dh0", f32, n), a.lens(lens)), stream)
@@ -180,8 +177,8 @@ def _norm_params(cfg) -> int:
 def gdn_group_norm(cfg, x, w, y, b=None, z=None, lens=None, stream=None):
     """x, y and the gate z act [B][L][H][D]; w and the bias b fp32 [D] or [H][D]; lens int32 [B]."""
     a, act, n = _Args(cfg, x), _TORCH_DT[cfg.act_dtype], _norm_params(cfg)
-    a.call("gdn_group_norm", (
-        byref(cfg), a.shape[1], a.tokens(x, "x", act), a.dense(w, "w", torch.float32, n),
+    a.call("gdn_group_norm", cfg, (
+        a.tokens(x, "x", act), a.dense(w, "w", torch.float32, n),
         a.dense(b, "b", torch.float32, n), a.tokens(z, "z", act), a.tokens(y, "y", act),
         a.lens(lens)), stream)
 
@@ -196,12 +193,12 @@ def gdn_group_norm_backward(cfg, x, w, dy, dx, dw, b=None, z=None, dz=None, db=N
     goes with z and db with b. workspace: at least
     gdn_group_norm_backward_workspace_bytes(cfg, L) bytes on the device, made here when None."""
     a, act, n = _Args(cfg, x), _TORCH_DT[cfg.act_dtype], _norm_params(cfg)
-    f32, L = torch.float32, a.shape[1]
-    a.call("gdn_group_norm_backward", (
-        byref(cfg), L, a.tokens(x, "x", act), a.dense(w, "w", f32, n), a.dense(b, "b", f32, n),
+    f32 = torch.float32
+    a.call("gdn_group_norm_backward", cfg, (
+        a.tokens(x, "x", act), a.dense(w, "w", f32, n), a.dense(b, "b", f32, n),
         a.tokens(z, "z", act), a.tokens(dy, "dy", act), a.tokens(dx, "dx", act),
         a.tokens(dz, "dz", act), a.dense(dw, "dw", f32, n), a.dense(db, "db", f32, n),
-        a.lens(lens)), stream, workspace, gdn_group_norm_backward_workspace_bytes(cfg, L))
+        a.lens(lens)), stream, workspace, gdn_group_norm_backward_workspace_bytes)
 
 
 def gdn_short_conv(cfg, x, w, y, bias=None, state_in=None, state_out=None, lens=None,
@@ -210,8 +207,8 @@ def gdn_short_conv(cfg, x, w, y, bias=None, state_in=None, state_out=None, lens=
     [B][K-1][H][D], the inputs before the first token and the last ones; lens int32 [B]."""
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
     C, n = cfg.H * cfg.D, cfg.B * (cfg.K - 1) * cfg.H * cfg.D
-    a.call("gdn_short_conv", (
-        byref(cfg), a.shape[1], a.tokens(x, "x", act), a.dense(w, "w", torch.float32, C * cfg.K),
+    a.call("gdn_short_conv", cfg, (
+        a.tokens(x, "x", act), a.dense(w, "w", torch.float32, C * cfg.K),
         a.dense(bias, "bias", torch.float32, C), a.dense(state_in, "state_in", act, n),
         a.tokens(y, "y", act), a.dense(state_out, "state_out", act, n), a.lens(lens)), stream)
 
@@ -229,11 +226,11 @@ def gdn_short_conv_backward(cfg, x, w, dy, dx, dw, bias=None, db=None, state_in=
     None."""
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
     C, n = cfg.H * cfg.D, cfg.B * (cfg.K - 1) * cfg.H * cfg.D
-    f32, L = torch.float32, a.shape[1]
-    a.call("gdn_short_conv_backward", (
-        byref(cfg), L, a.tokens(x, "x", act), a.dense(w, "w", f32, C * cfg.K),
+    f32 = torch.float32
+    a.call("gdn_short_conv_backward", cfg, (
+        a.tokens(x, "x", act), a.dense(w, "w", f32, C * cfg.K),
         a.dense(bias, "bias", f32, C), a.dense(state_in, "state_in", act, n),
         a.tokens(dy, "dy", act), a.dense(dstate_out, "dstate_out", act, n),
         a.tokens(dx, "dx", act), a.dense(dw, "dw", f32, C * cfg.K), a.dense(db, "db", f32, C),
         a.dense(dstate_in, "dstate_in", act, n), a.lens(lens)), stream, workspace,
-        gdn_short_conv_backward_workspace_bytes(cfg, L))
+        gdn_short_conv_backward_workspace_bytes)
