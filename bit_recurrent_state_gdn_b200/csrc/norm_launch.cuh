@@ -82,7 +82,8 @@ cudaError_t norm_pieces(const NormArgs& a, cudaStream_t st) {
     return norm_go<Act, GATE, BACKWARD, PiecesInRegisters<Act, LANES, NI, N>>(a, st);
   else
     return norm_go<Act, GATE, BACKWARD,
-                   PiecesInShared<Act, V, LANES, NI, N, norm_stages(NI * V * (int)sizeof(Act), BACKWARD)>>(a, st);
+                   PiecesInShared<Act, V, LANES, NI, N, norm_stages(NI * V * (int)sizeof(Act), BACKWARD),
+                                  !BACKWARD>>(a, st);
 }
 
 template <typename Act, bool BACKWARD, int NI>
