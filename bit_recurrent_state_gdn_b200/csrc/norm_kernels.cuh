@@ -11,8 +11,10 @@
 // and the sums for their gradients do too, and walks tokens; these sums are joined over the CTA
 // in shared memory, written as partial sums, and added by a second kernel in a fixed order.
 //
-// Bound by HBM: rows come through a ring in shared memory, S rows ahead, each lane copying the
-// pieces that it will read (no barrier in the loop).
+// Bound by HBM, and close to it by instructions: rows come through a ring in shared memory, S rows
+// ahead, each lane copying the pieces that it will read (no barrier in the loop). bf16, rows of 128
+// with a gate, of 6452 GB/s: forward 8 x 32 x 4096 tokens 138 us, 5.9 TB/s (24 instructions per
+// element); backward 4 x 32 x 4096 119 us, 5.6 TB/s (38).
 #pragma once
 
 #include <type_traits>
@@ -353,6 +355,7 @@ __global__ void __launch_bounds__(kNormThreads, MINB) norm_kernel(NormArgs a, No
     at.next(a.L);
     y_at.next(at);
   }
+  asm volatile("cp.async.wait_all;\n" ::: "memory");  // copies behind the last row
 }
 
 // Shared memory: the ring, then (the loop done) two floats for every channel that a lane holds.

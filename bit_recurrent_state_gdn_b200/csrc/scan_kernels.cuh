@@ -210,7 +210,8 @@ __device__ __forceinline__ void state_store(float* p, bool both, F2 f) {
 
 // The tokens of a warp's runs, tile after tile, as the scans read them: gate, input and (backward)
 // the gradient of the output. start() begins with the run at t0, `step` tokens from one tile to
-// the next; take() makes the next run readable; next() may begin the loads after it.
+// the next; take() makes the next run readable; next() may begin the loads after it; finish() waits for what is still
+// under way.
 //
 // RunsInRegisters: any alignment, one tile ahead in registers.
 template <typename Act, int STEP, int T, bool BACKWARD>
@@ -258,6 +259,7 @@ struct RunsInRegisters {
     }
   }
   __device__ __forceinline__ void next() { fetch(); }  // once the gates have been read
+  __device__ __forceinline__ void finish() {}
   __device__ __forceinline__ F2 g(int j) const { return next_g[j].get(); }
   __device__ __forceinline__ F2 x(int j) const { return now_x[j].get(); }
   __device__ __forceinline__ F2 grad_o(int j) const { return now_d[j].get(); }
@@ -338,6 +340,7 @@ struct RunsInShared {
     fetch();
   }
   __device__ __forceinline__ void next() {}
+  __device__ __forceinline__ void finish() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
   __device__ __forceinline__ F2 g(int j) const {
     return reinterpret_cast<const Raw<float, 1>*>(now)[j * 32 + (threadIdx.x & 31)].get();
   }
@@ -463,6 +466,7 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
     }
     if constexpr (W == 1) carry = h;
   }
+  runs.finish();  // copies behind the last tile
   if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);
 }
 
@@ -587,6 +591,7 @@ __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
       }
     }
   }
+  runs.finish();  // copies behind the last tile
   if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);
 }
 
