@@ -37,8 +37,8 @@ cudaError_t launch_conv_reduce(const ConvArgs& a, int parts, cudaStream_t st) {
 // Large enough for any placement of the arrays, on which the split depends.
 size_t conv_backward_workspace(const gdn_conv_config& cfg, int L) {
   const int C = cfg.H * cfg.D;
-  const int parts = std::max(conv_backward_split(cfg.B, L, C, kConvBackVec).parts,
-                             conv_backward_split(cfg.B, L, C, 1).parts);
+  int parts = 1;
+  for (const int V : {1, 2, kConvBackVec}) parts = std::max(parts, conv_backward_split(cfg.B, L, C, V).parts);
   return (size_t)parts * (size_t)C * (size_t)(cfg.K + 1) * sizeof(float);
 }
 

@@ -470,26 +470,28 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
   if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);
 }
 
-// A CTA's tile is one chunk between kept states.
-template <typename Act, int SCALE, class Runs, int CL, int MINB>
-__global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
-    scan_backward_kernel(ScanArgs a, int slabs) {
-  constexpr int T = Runs::kTokens, W = GDN_SCAN_CHUNK / T;
-  constexpr int STEP = Runs::kStep;
+// A CTA's tile is one chunk between kept states; with one warp a unit (sequences of one run) eight
+// units share a CTA.
+template <typename Act, int SCALE, class Runs, int W, int CL, int MINB>
+__global__ void __launch_bounds__(scan_threads(W), MINB) scan_backward_kernel(ScanArgs a, int slabs) {
+  constexpr int T = Runs::kTokens, STEP = Runs::kStep, kGroups = scan_groups(W);
+  static_assert(W * T == GDN_SCAN_CHUNK || (W == 1 && CL == 1), "tiles begin at kept states");
   extern __shared__ __align__(128) uint8_t rings[];
-  __shared__ alignas(16) Link agg[2][W][32];  // decay and forward scan of each run
-  __shared__ F2 agg_back[2][W][32];           // its scan of the gradient
+  __shared__ alignas(16) Link agg[W > 1 ? 2 : 1][W][W > 1 ? 32 : 1];  // decay and scan of each run
+  __shared__ F2 agg_back[W > 1 ? 2 : 1][W][W > 1 ? 32 : 1];           // its scan of the gradient
   __shared__ alignas(16) Link across[CL > 1 ? 2 : 1][CL][CL > 1 ? 32 : 1];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = W > 1 ? threadIdx.x >> 5 : 0;
   const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
-  const int64_t unit = blockIdx.x / CL;
+  const int64_t unit = CL > 1 ? blockIdx.x / CL
+                              : (int64_t)blockIdx.x * kGroups + (W > 1 ? 0 : threadIdx.x >> 5);
+  if (W == 1 && unit >= (int64_t)a.B * slabs) return;  // no barrier waits for this warp
   const int b = (int)(unit / slabs), slab = (int)(unit % slabs);
   const ScanLane me = scan_lane<STEP>(a, slab);
   const bool live = me.live;
   const int len = seq_len(a.lens, b, a.L);
   const Column<Act, STEP> gx(a.grad_x, b, me);
   const Column<float, STEP> gg(a.grad_g, b, me);
-  Runs runs(a, rings + w * Runs::kBytes, b, slab, len);
+  Runs runs(a, rings + (threadIdx.x >> 5) * Runs::kBytes, b, slab, len);
   const int64_t state = (int64_t)b * a.C + me.c;
   const float* hist =
       a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + me.c;
@@ -503,9 +505,9 @@ __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
                : f2_all(0.0f);
   };
 
-  constexpr int kTile = CL * GDN_SCAN_CHUNK;
+  constexpr int kTile = CL * W * T;
   const int tiles = (len + kTile - 1) / kTile;
-  int t0 = (tiles - 1) * kTile + rank * GDN_SCAN_CHUNK + w * T;
+  int t0 = (tiles - 1) * kTile + (rank * W + w) * T;
   runs.start(t0, -kTile);
   F2 next_h = kept(t0 - w * T);
   if constexpr (CL > 1) cluster_barrier();  // every CTA of the cluster runs before it is written to
@@ -527,43 +529,45 @@ __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
     for (int j = T - 1; j >= 0; --j) bwd = f2_mul(at[j], f2_add(runs.grad_o(j), bwd));
     runs.next();
     next_h = kept(t0 - w * T - kTile);
-    agg[buf][w][lane] = Link{run_decay(g_sum), fwd};
-    agg_back[buf][w][lane] = bwd;
-    __syncthreads();
     F2 dc = carry;  // the gradient that reaches the warp's last state from behind
-    if constexpr (CL > 1) {
-      // the CTA's run, and the part of it behind this warp's
-      Link behind = {f2_all(1.0f), f2_all(0.0f)}, all = behind;
+    if constexpr (W > 1) {
+      agg[buf][w][lane] = Link{run_decay(g_sum), fwd};
+      agg_back[buf][w][lane] = bwd;
+      __syncthreads();
+      if constexpr (CL > 1) {
+        // the CTA's run, and the part of it behind this warp's
+        Link behind = {f2_all(1.0f), f2_all(0.0f)}, all = behind;
 #pragma unroll
-      for (int i = W - 1; i >= 0; --i) {
-        if (i == w) behind = all;
-        const F2 ai = agg[buf][i][lane].a;
-        all.a = f2_mul(ai, all.a);
-        all.b = f2_fma(ai, all.b, agg_back[buf][i][lane]);
-      }
-      for (int r = w; r < CL; r += W) cluster_store(&across[buf][rank][lane], r, all);
+        for (int i = W - 1; i >= 0; --i) {
+          if (i == w) behind = all;
+          const F2 ai = agg[buf][i][lane].a;
+          all.a = f2_mul(ai, all.a);
+          all.b = f2_fma(ai, all.b, agg_back[buf][i][lane]);
+        }
+        for (int r = w; r < CL; r += W) cluster_store(&across[buf][rank][lane], r, all);
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) {
-        const Link l = agg[buf][i][lane];
-        if (i < w) h = f2_fma(l.a, h, l.b);
-      }
-      cluster_barrier();
+        for (int i = 0; i < W - 1; ++i) {
+          const Link l = agg[buf][i][lane];
+          if (i < w) h = f2_fma(l.a, h, l.b);
+        }
+        cluster_barrier();
 #pragma unroll
-      for (int i = CL - 1; i >= 0; --i) {
-        if (i == rank) dc = f2_fma(behind.a, carry, behind.b);
-        const Link l = across[buf][i][lane];
-        carry = f2_fma(l.a, carry, l.b);
-      }
-    } else {
+        for (int i = CL - 1; i >= 0; --i) {
+          if (i == rank) dc = f2_fma(behind.a, carry, behind.b);
+          const Link l = across[buf][i][lane];
+          carry = f2_fma(l.a, carry, l.b);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) {
-        const Link l = agg[buf][i][lane];
-        if (i < w) h = f2_fma(l.a, h, l.b);
-      }
+        for (int i = 0; i < W - 1; ++i) {
+          const Link l = agg[buf][i][lane];
+          if (i < w) h = f2_fma(l.a, h, l.b);
+        }
 #pragma unroll
-      for (int i = W - 1; i >= 0; --i) {
-        if (i == w) dc = carry;
-        carry = f2_fma(agg[buf][i][lane].a, carry, agg_back[buf][i][lane]);
+        for (int i = W - 1; i >= 0; --i) {
+          if (i == w) dc = carry;
+          carry = f2_fma(agg[buf][i][lane].a, carry, agg_back[buf][i][lane]);
+        }
       }
     }
     F2 before[T];  // the state before each token, and what the slope of s adds to it
@@ -590,6 +594,7 @@ __global__ void __launch_bounds__(32 * (GDN_SCAN_CHUNK / Runs::kTokens), MINB)
         wg.store(j, f2_mul(dc, before[j]));
       }
     }
+    if constexpr (W == 1) carry = dc;
   }
   runs.finish();  // copies behind the last tile
   if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);

@@ -37,13 +37,15 @@ cudaError_t scan_forward(const ScanArgs& a, int slabs, cudaStream_t st) {
   return launch_in_clusters(kernel, grid, kThreads, CL, kShared, st, a, slabs);
 }
 
-template <typename Act, int SCALE, class Runs, int CL, int MINB>
+template <typename Act, int SCALE, class Runs, int W, int CL, int MINB>
 cudaError_t scan_back(const ScanArgs& a, int slabs, cudaStream_t st) {
-  constexpr auto kernel = scan_backward_kernel<Act, SCALE, Runs, CL, MINB>;
-  constexpr int W = GDN_SCAN_CHUNK / Runs::kTokens, kShared = W * Runs::kBytes;
+  constexpr auto kernel = scan_backward_kernel<Act, SCALE, Runs, W, CL, MINB>;
+  constexpr int kThreads = scan_threads(W), kShared = kThreads / 32 * Runs::kBytes;
   const cudaError_t e = ensure_smem<kernel>(kShared ? std::max(kShared, 48 * 1024 + 16) : 0);
   if (e != cudaSuccess) return e;
-  return launch_in_clusters(kernel, (int64_t)a.B * slabs * CL, 32 * W, CL, kShared, st, a, slabs);
+  const int64_t units = (int64_t)a.B * slabs;
+  const int64_t grid = (units + scan_groups(W) - 1) / scan_groups(W) * CL;
+  return launch_in_clusters(kernel, grid, kThreads, CL, kShared, st, a, slabs);
 }
 
 // CTAs that share a unit (a slab of channels of one sequence) as a cluster: where units are
@@ -74,15 +76,20 @@ cudaError_t launch_scan_plan(const ScanArgs& a, bool backward, cudaStream_t st) 
   const int slabs = (a.C + kScanSlab - 1) / kScanSlab;
   const int64_t units = (int64_t)a.B * slabs;
   if (backward) {
+    // sequences of one run need no joins (52 x 2150 channels, 1 token: 35 us with a CTA each)
+    if (a.L <= P::BackAlone::kTokens)
+      return scan_back<Act, SCALE, typename P::BackAlone, 1, 1, 1>(a, slabs, st);
+    using Back = typename P::Back;
+    constexpr int W = GDN_SCAN_CHUNK / Back::kTokens, kResident = P::kBackResident;
     switch (scan_cluster(units, GDN_SCAN_CHUNK, a.L)) {
       case 1:
-        return scan_back<Act, SCALE, typename P::Back, 1, P::kBackResident>(a, slabs, st);
+        return scan_back<Act, SCALE, Back, W, 1, kResident>(a, slabs, st);
       case 2:
-        return scan_back<Act, SCALE, typename P::Back, 2, P::kBackResident>(a, slabs, st);
+        return scan_back<Act, SCALE, Back, W, 2, kResident>(a, slabs, st);
       case 4:
-        return scan_back<Act, SCALE, typename P::Back, 4, P::kBackResident>(a, slabs, st);
+        return scan_back<Act, SCALE, Back, W, 4, kResident>(a, slabs, st);
       default:
-        return scan_back<Act, SCALE, typename P::Back, 8, P::kBackResident>(a, slabs, st);
+        return scan_back<Act, SCALE, Back, W, 8, kResident>(a, slabs, st);
     }
   }
   if (a.L <= 1) return scan_forward<Act, SCALE, typename P::One, 1, 1, 4>(a, slabs, st);
@@ -116,6 +123,7 @@ struct PlanShared {
   using Four = RunsInShared<Act, 16, 2, false>;
   using Eight = RunsInShared<Act, kF32 ? 8 : 16, kF32 ? 3 : 2, false>;
   using Back = RunsInShared<Act, 16, 2, true>;
+  using BackAlone = RunsInRegisters<Act, 1, 8, true>;
   static constexpr int kBackResident = 2;
 };
 
@@ -127,6 +135,7 @@ struct PlanRegisters {
   using Four = Alone;
   using Eight = Alone;
   using Back = RunsInRegisters<Act, STEP, 8, true>;
+  using BackAlone = Back;
   static constexpr int kBackResident = 1;  // two spill (3875 channels, 8 x 1000 tokens: 1.5 / 2.2 TB/s)
 };
 

@@ -94,6 +94,10 @@ SCAN = [
     (64, 100, 32, 64, "bf16", "complement", "tokens", [100, 3] * 32),
     (15, 1100, 4, 64, "bf16", "sqrt", "tokens", [1100, 0, 513] * 5),
     (20, 300, 4, 64, "f32", "sqrt", "wide", [300, 128, 129, 1] * 5),
+    # sequences of one run, many of them
+    (52, 1, 5, 43, "bf16", "complement", "wide", [1, 0, 1, 1] * 13),
+    (33, 8, 2, 64, "bf16", "sqrt", "heads", None),
+    (33, 5, 3, 33, "f32", "sqrt", "odd", [5, 0, 3] * 11),
 ]
 
 
@@ -376,6 +380,10 @@ CONV = [
     (2100, 1, 16, 128, "bf16", 4, True, "silu", "tokens", [1, 1, 0] * 700),
     (2100, 1, 3, 50, "f32", 2, False, "silu", "tokens", None),
     (1, 5000, 1, 64, "bf16", 4, True, "silu", "tokens", None),
+    # few channels
+    (5, 300, 1, 32, "bf16", 3, True, "silu", "wide", [300, 299, 0, 1, 40]),
+    (3, 200, 2, 7, "bf16", 4, True, "silu", "heads", None),
+    (2, 200, 1, 26, "f32", 4, True, "none", "tokens", None),
 ]
 
 
