@@ -32,6 +32,7 @@ from .prefill import gdn_prefill, gdn_prefill_workspace_bytes  # noqa: F401,E402
 from .layer import (  # noqa: F401,E402
     gdn_gated_scan,
     gdn_gated_scan_backward,
+    gdn_gated_scan_workspace_bytes,
     gdn_group_norm,
     gdn_group_norm_backward,
     gdn_group_norm_backward_workspace_bytes,

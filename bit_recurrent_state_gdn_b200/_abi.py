@@ -20,6 +20,7 @@ GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1, 2
 GDN_SCALE_NONE, GDN_SCALE_COMPLEMENT, GDN_SCALE_SQRT = 0, 1, 2
 GDN_WEIGHT_HEAD, GDN_WEIGHT_CHANNEL = 0, 1
 GDN_SCAN_CHUNK = 64
+GDN_SCAN_SPLIT = 4096
 GDN_NORM_MAX_D = 8192
 GDN_CONV_MAX_K = 4
 
@@ -114,8 +115,10 @@ SIGNATURES = {
     "gdn_pw_materialize": (_i32, [_PWC, _PWS, _vp, _vp]),
     "gdn_prefill": (_i32, [ctypes.POINTER(gdn_config), _i32] + [_vp] * 8 + [_sz, _vp]),
     "gdn_prefill_workspace_bytes": (_sz, [ctypes.POINTER(gdn_config), _i32]),
-    "gdn_gated_scan": (_i32, [_SC, _i32, _TK, _TK, _TK] + [_vp] * 5),
-    "gdn_gated_scan_backward": (_i32, [_SC, _i32, _TK, _TK, _vp, _TK, _vp, _TK, _TK] + [_vp] * 3),
+    "gdn_gated_scan": (_i32, [_SC, _i32, _TK, _TK, _TK] + [_vp] * 5 + [_sz, _vp]),
+    "gdn_gated_scan_backward": (_i32, [_SC, _i32, _TK, _TK, _vp, _TK, _vp, _TK, _TK] + [_vp] * 3
+                                + [_sz, _vp]),
+    "gdn_gated_scan_workspace_bytes": (_sz, [_SC, _i32]),
     "gdn_group_norm": (_i32, [_NC, _i32, _TK, _vp, _vp, _TK, _TK, _vp, _vp]),
     "gdn_group_norm_backward": (_i32, [_NC, _i32, _TK, _vp, _vp, _TK, _TK, _TK, _TK]
                                 + [_vp] * 4 + [_sz, _vp]),

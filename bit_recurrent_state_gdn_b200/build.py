@@ -21,7 +21,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdnq.so")
 SOURCES = ["api.cu", "window_int8.cu", "window_int4.cu", "window_mixed.cu", "window_int8_smooth.cu",
            "window_int4_smooth.cu", "baseline.cu",
-           "pw.cu", "prefill.cu", "layer_api.cu", "scan_bf16.cu", "scan_f32.cu", "norm.cu",
+           "pw.cu", "prefill.cu", "layer_api.cu", "scan.cu", "scan_bf16.cu", "scan_f32.cu", "norm.cu",
            "norm_bf16_forward.cu", "norm_bf16_backward.cu", "norm_f32_forward.cu",
            "norm_f32_backward.cu", "conv.cu", "conv_bf16.cu", "conv_f32.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -180,9 +180,19 @@ gdn_status zero(float* p, size_t n, gdn_stream_t stream, const char* where) {
 
 extern "C" {
 
+size_t gdn_gated_scan_workspace_bytes(const gdn_scan_config* cfg, int32_t L) {
+  clear_error();
+  Shape s;
+  if (check_scan(cfg, L, &s) != GDN_OK || s.empty()) return 0;
+  gdnq::ScanArgs a{};
+  a.B = cfg->B, a.L = L, a.C = cfg->H * cfg->D;
+  return gdnq::scan_spans(a);
+}
+
 gdn_status gdn_gated_scan(const gdn_scan_config* cfg, int32_t L, const gdn_tokens* x,
                           const gdn_tokens* g, const gdn_tokens* o, const float* h0, float* hT,
-                          float* hist, const int32_t* lens, gdn_stream_t stream) {
+                          float* hist, const int32_t* lens, void* workspace,
+                          size_t workspace_bytes, gdn_stream_t stream) {
   clear_error();
   Shape s;
   GDNQ_TRY(check_scan(cfg, L, &s));
@@ -203,6 +213,9 @@ gdn_status gdn_gated_scan(const gdn_scan_config* cfg, int32_t L, const gdn_token
   a.x = tok(x), a.g = tok(g), a.o = tok(o);
   a.h0 = h0, a.hT = hT, a.hist = hist, a.lens = lens;
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D;
+  const size_t need = gdnq::scan_spans(a);
+  GDNQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  a.spans = need > 0 ? workspace : nullptr;
   const cudaError_t err = launch_scan(a, cfg, false, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_gated_scan");
 }
@@ -211,7 +224,8 @@ gdn_status gdn_gated_scan_backward(const gdn_scan_config* cfg, int32_t L, const 
                                    const gdn_tokens* g, const float* hist,
                                    const gdn_tokens* grad_o, const float* grad_hT,
                                    const gdn_tokens* grad_x, const gdn_tokens* grad_g,
-                                   float* grad_h0, const int32_t* lens, gdn_stream_t stream) {
+                                   float* grad_h0, const int32_t* lens, void* workspace,
+                                   size_t workspace_bytes, gdn_stream_t stream) {
   clear_error();
   Shape s;
   GDNQ_TRY(check_scan(cfg, L, &s));
@@ -242,6 +256,9 @@ gdn_status gdn_gated_scan_backward(const gdn_scan_config* cfg, int32_t L, const 
   a.grad_o = tok(grad_o), a.grad_x = tok(grad_x), a.grad_g = tok(grad_g);
   a.h0 = grad_hT, a.hT = grad_h0, a.hist = const_cast<float*>(hist), a.lens = lens;
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D;
+  const size_t need = gdnq::scan_spans(a);
+  GDNQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  a.spans = need > 0 ? workspace : nullptr;
   const cudaError_t err = launch_scan(a, cfg, true, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_gated_scan_backward");
 }

@@ -22,6 +22,9 @@ struct ScanArgs {
   float* hist;            // written forward, read backward
   const int32_t* lens;
   int B, L, H, D, C;      // C = H D
+  void* spans;            // workspace: what each span of a split sequence does to the state
+  int span_tokens;        // tokens of a span; spans per sequence
+  int spans_per_unit;
 };
 
 struct NormArgs {
@@ -85,6 +88,8 @@ cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, int threads,
 // Forward or backward scan, by activation type; scale is a gdn_input_scale.
 cudaError_t launch_scan_f32(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
 cudaError_t launch_scan_bf16(const ScanArgs& a, int scale, bool backward, cudaStream_t st);
+// Fills in span_tokens and spans_per_unit, and returns the bytes of `spans` (0: not split).
+size_t scan_spans(ScanArgs& a);
 cudaError_t launch_norm_f32_forward(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_f32_backward(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_bf16_forward(const NormArgs& a, cudaStream_t st);

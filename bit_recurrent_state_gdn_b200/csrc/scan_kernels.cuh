@@ -373,8 +373,95 @@ __device__ __forceinline__ void cluster_store(Link* p, int rank, Link v) {
 constexpr int scan_groups(int W) { return W == 1 ? 8 : 1; }
 constexpr int scan_threads(int W) { return 32 * W * scan_groups(W); }
 
-template <typename Act, int SCALE, class Runs, int W, int CL, int MINB>
+// Few sequences of many tokens: each is split into spans, which CTAs of their own take side by side.
+// A first kernel leaves what every span does to the state; a span's state is then what the spans
+// before it (backward, behind it) make of the sequence's. It reads a part of the data twice, where
+// one chain of clusters would leave most of the machine idle.
+// Link 0 of a unit is its first state (forward), link i + 1 span i's.
+__device__ __forceinline__ Link* span_links(const ScanArgs& a, int64_t units, int64_t unit, int link) {
+  return static_cast<Link*>(a.spans) + (link * units + unit) * 32 + (threadIdx.x & 31);
+}
+
+__device__ __forceinline__ Link join(const Link& first, const Link& then) {
+  return Link{f2_mul(then.a, first.a), f2_fma(then.a, first.b, then.b)};
+}
+
+// The links from `from` on, `count` of them in steps of `step`, joined in that order: an equal part
+// by each of the CTA's W warps, the parts in shared memory. The same in every warp.
+template <int W>
+__device__ __forceinline__ Link join_spans(const ScanArgs& a, int64_t units, int64_t unit, int from,
+                                           int count, int step, Link (*shared)[32]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int share = (count + W - 1) / W, begin = w * share, end = min(begin + share, count);
+  Link all = {f2_all(1.0f), f2_all(0.0f)};
+#pragma unroll 8
+  for (int i = begin; i < end; ++i) all = join(all, *span_links(a, units, unit, from + i * step));
+  shared[w][lane] = all;
+  __syncthreads();
+  all = shared[0][lane];
+#pragma unroll
+  for (int i = 1; i < W; ++i) all = join(all, shared[i][lane]);
+  __syncthreads();
+  return all;
+}
+
+// A warp takes an eighth of a span. Backward `in` is grad_o, and a run acts on the gradient that
+// comes from behind.
+template <typename Act, int SCALE, class Runs, bool BACKWARD>
+__global__ void __launch_bounds__(256, 2) scan_span_kernel(ScanArgs a, int slabs) {
+  constexpr int W = 8, T = Runs::kTokens;
+  extern __shared__ __align__(128) uint8_t rings[];
+  __shared__ alignas(16) Link part[W][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t units = (int64_t)a.B * slabs, unit = blockIdx.x % units;
+  const int span = (int)(blockIdx.x / units);
+  const int b = (int)(unit / slabs), slab = (int)(unit % slabs);
+  const int len = seq_len(a.lens, b, a.L), first = span * a.span_tokens;
+  if (!BACKWARD && span == 0 && w == 0) {
+    // the state before the sequence: the second kernel's CTAs read it here, since hT may be h0
+    const ScanLane me = scan_lane<Runs::kStep>(a, slab);
+    const int64_t state = (int64_t)b * a.C + me.c;
+    *span_links(a, units, unit, 0) = Link{
+        f2_all(0.0f), a.h0 && me.live ? state_load<Runs::kStep>(a.h0 + state, me.both) : f2_all(0.0f)};
+  }
+  if (first >= len) return;
+  const int share = a.span_tokens / W, begin = first + w * share, end = min(begin + share, len);
+  Runs runs(a, rings + w * Runs::kBytes, b, slab, end);
+  const int tiles = end > begin ? (end - begin + T - 1) / T : 0;
+  runs.start(BACKWARD ? begin + (tiles - 1) * T : begin, BACKWARD ? -T : T);
+  Link all = {f2_all(1.0f), f2_all(0.0f)};
+  for (int tile = 0; tile < tiles; ++tile) {
+    runs.take();
+    F2 g_sum = f2_all(0.0f), at[T];
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const F2 gj = runs.g(j);
+      const Gate q = gate_of<BACKWARD ? GDN_SCALE_NONE : SCALE>(gj);
+      at[j] = q.a;
+      g_sum = f2_add(g_sum, gj);
+      if constexpr (!BACKWARD) all.b = f2_fma(q.a, all.b, f2_mul(q.s, runs.x(j)));
+    }
+    if constexpr (BACKWARD) {
+#pragma unroll
+      for (int j = T - 1; j >= 0; --j) all.b = f2_mul(at[j], f2_add(runs.x(j), all.b));
+    }
+    all.a = f2_mul(all.a, run_decay(g_sum));
+    runs.next();
+  }
+  runs.finish();
+  part[w][lane] = all;
+  __syncthreads();
+  if (w == 0) {
+    all = part[BACKWARD ? W - 1 : 0][lane];
+#pragma unroll
+    for (int i = 1; i < W; ++i) all = join(all, part[BACKWARD ? W - 1 - i : i][lane]);
+    *span_links(a, units, unit, span + 1) = all;
+  }
+}
+
+template <typename Act, int SCALE, class Runs, int W, int CL, int MINB, bool SPLIT = false>
 __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a, int slabs) {
+  static_assert(!SPLIT || (CL == 1 && W > 1), "a span is one CTA's");
   constexpr int kGroups = scan_groups(W), STEP = Runs::kStep, T = Runs::kTokens;
   extern __shared__ __align__(128) uint8_t rings[];
   static_assert(GDN_SCAN_CHUNK % T == 0, "kept states stand where runs begin");
@@ -382,27 +469,37 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
   __shared__ alignas(16) Link across[CL > 1 ? 2 : 1][CL][CL > 1 ? 32 : 1];
   const int lane = threadIdx.x & 31, w = W > 1 ? threadIdx.x >> 5 : 0;
   const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
-  const int64_t unit = CL > 1 ? blockIdx.x / CL
-                              : (int64_t)blockIdx.x * kGroups + (W > 1 ? 0 : threadIdx.x >> 5);
+  const int64_t units = SPLIT ? (int64_t)a.B * slabs : 0;
+  const int span = SPLIT ? (int)(blockIdx.x / units) : 0;
+  const int64_t unit = SPLIT ? blockIdx.x % units
+                       : CL > 1 ? blockIdx.x / CL
+                                : (int64_t)blockIdx.x * kGroups + (W > 1 ? 0 : threadIdx.x >> 5);
   if (W == 1 && unit >= (int64_t)a.B * slabs) return;  // no barrier waits for this warp
   const int b = (int)(unit / slabs), slab = (int)(unit % slabs);
   const ScanLane me = scan_lane<STEP>(a, slab);
   const bool live = me.live;
-  const int len = seq_len(a.lens, b, a.L);
+  const int length = seq_len(a.lens, b, a.L);
+  const int first = SPLIT ? span * a.span_tokens : 0;
+  if (SPLIT && span > 0 && first >= length) return;
+  const int len = SPLIT ? min(length, first + a.span_tokens) : length;  // this CTA's end
   const Column<Act, STEP> o(a.o, b, me);
   Runs runs(a, rings + (threadIdx.x >> 5) * Runs::kBytes, b, slab, len);
   const int64_t state = (int64_t)b * a.C + me.c;
   float* hist = a.hist && live
                     ? a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + me.c
                     : nullptr;
-  F2 carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);  // before the tile
+  F2 carry;  // before the tile
+  if constexpr (SPLIT)
+    carry = join_spans<W>(a, units, unit, 0, span + 1, 1, agg[0]).b;
+  else
+    carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);
 
   constexpr int kTile = CL * W * T;
-  int t0 = (rank * W + w) * T;
+  int t0 = first + (rank * W + w) * T;
   runs.start(t0, kTile);
   if constexpr (CL > 1) cluster_barrier();  // every CTA of the cluster runs before it is written to
   int buf = 0;
-  for (int tile = 0; tile < len; tile += kTile, t0 += kTile, buf ^= 1) {
+  for (int tile = first; tile < len; tile += kTile, t0 += kTile, buf ^= 1) {
     runs.take();
     F2 at[T], u[T], g_sum = f2_all(0.0f), local = f2_all(0.0f);
 #pragma unroll
@@ -467,12 +564,12 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
     if constexpr (W == 1) carry = h;
   }
   runs.finish();  // copies behind the last tile
-  if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);
+  if (a.hT && live && rank == 0 && w == 0 && len == length) state_store<STEP>(a.hT + state, me.both, carry);
 }
 
 // A CTA's tile is one chunk between kept states; with one warp a unit (sequences of one run) eight
 // units share a CTA.
-template <typename Act, int SCALE, class Runs, int W, int CL, int MINB>
+template <typename Act, int SCALE, class Runs, int W, int CL, int MINB, bool SPLIT = false>
 __global__ void __launch_bounds__(scan_threads(W), MINB) scan_backward_kernel(ScanArgs a, int slabs) {
   constexpr int T = Runs::kTokens, STEP = Runs::kStep, kGroups = scan_groups(W);
   static_assert(W * T == GDN_SCAN_CHUNK || (W == 1 && CL == 1), "tiles begin at kept states");
@@ -482,13 +579,19 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_backward_kernel(Sc
   __shared__ alignas(16) Link across[CL > 1 ? 2 : 1][CL][CL > 1 ? 32 : 1];
   const int lane = threadIdx.x & 31, w = W > 1 ? threadIdx.x >> 5 : 0;
   const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
-  const int64_t unit = CL > 1 ? blockIdx.x / CL
-                              : (int64_t)blockIdx.x * kGroups + (W > 1 ? 0 : threadIdx.x >> 5);
+  const int64_t units = SPLIT ? (int64_t)a.B * slabs : 0;
+  const int span = SPLIT ? (int)(blockIdx.x / units) : 0;
+  const int64_t unit = SPLIT ? blockIdx.x % units
+                       : CL > 1 ? blockIdx.x / CL
+                                : (int64_t)blockIdx.x * kGroups + (W > 1 ? 0 : threadIdx.x >> 5);
   if (W == 1 && unit >= (int64_t)a.B * slabs) return;  // no barrier waits for this warp
   const int b = (int)(unit / slabs), slab = (int)(unit % slabs);
   const ScanLane me = scan_lane<STEP>(a, slab);
   const bool live = me.live;
-  const int len = seq_len(a.lens, b, a.L);
+  const int length = seq_len(a.lens, b, a.L);
+  const int begin = SPLIT ? span * a.span_tokens : 0;
+  if (SPLIT && span > 0 && begin >= length) return;
+  const int len = SPLIT ? min(length, begin + a.span_tokens) : length;  // this CTA's end
   const Column<Act, STEP> gx(a.grad_x, b, me);
   const Column<float, STEP> gg(a.grad_g, b, me);
   Runs runs(a, rings + (threadIdx.x >> 5) * Runs::kBytes, b, slab, len);
@@ -498,16 +601,22 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_backward_kernel(Sc
   // the gradient that reaches the tile's last state from behind
   F2 carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);
 
+  if constexpr (SPLIT) {
+    const int last = (length + a.span_tokens - 1) / a.span_tokens;  // the last span's link
+    const Link l = join_spans<W>(a, units, unit, last, max(last - span - 1, 0), -1, agg[0]);
+    carry = f2_fma(l.a, carry, l.b);
+  }
+
   // the kept state before the CTA's tile that begins at `first`
   auto kept = [&](int first) {
-    return live && first >= 0 && first < len
+    return live && first >= begin && first < len
                ? state_load<STEP>(hist + (int64_t)(first / GDN_SCAN_CHUNK) * a.C, me.both)
                : f2_all(0.0f);
   };
 
   constexpr int kTile = CL * W * T;
-  const int tiles = (len + kTile - 1) / kTile;
-  int t0 = (tiles - 1) * kTile + (rank * W + w) * T;
+  const int tiles = (len - begin + kTile - 1) / kTile;
+  int t0 = begin + (tiles - 1) * kTile + (rank * W + w) * T;
   runs.start(t0, -kTile);
   F2 next_h = kept(t0 - w * T);
   if constexpr (CL > 1) cluster_barrier();  // every CTA of the cluster runs before it is written to
@@ -597,7 +706,7 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_backward_kernel(Sc
     if constexpr (W == 1) carry = dc;
   }
   runs.finish();  // copies behind the last tile
-  if (a.hT && live && rank == 0 && w == 0) state_store<STEP>(a.hT + state, me.both, carry);
+  if (a.hT && live && rank == 0 && w == 0 && span == 0) state_store<STEP>(a.hT + state, me.both, carry);
 }
 
 }  // namespace gdnq

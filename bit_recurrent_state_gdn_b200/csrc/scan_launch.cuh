@@ -71,10 +71,42 @@ inline ScanSplit scan_split(int64_t units, int L, int run) {
   return (units > 296 && units <= 592) || units > 1480 ? ScanSplit::Four : ScanSplit::Eight;
 }
 
+// The two kernels of sequences split into spans.
+template <typename Act, int SCALE, class P>
+cudaError_t launch_scan_split(ScanArgs a, bool backward, int slabs, cudaStream_t st) {
+  using Span = typename P::Alone;
+  const int64_t grid = (int64_t)a.B * slabs * a.spans_per_unit;
+  constexpr int kSpanShared = 8 * Span::kBytes;
+  constexpr int kRaised = kSpanShared ? std::max(kSpanShared, 48 * 1024 + 16) : 0;
+  if (backward) {
+    constexpr auto spans = scan_span_kernel<Act, SCALE, Span, true>;
+    cudaError_t e = ensure_smem<spans>(kRaised);
+    ScanArgs over = a;
+    over.x = a.grad_o;
+    if (e == cudaSuccess) e = launch_in_clusters(spans, grid, 256, 1, kSpanShared, st, over, slabs);
+    if (e != cudaSuccess) return e;
+    using Back = typename P::Back;
+    constexpr int W = GDN_SCAN_CHUNK / Back::kTokens, kShared = W * Back::kBytes;
+    constexpr auto kernel = scan_backward_kernel<Act, SCALE, Back, W, 1, P::kBackResident, true>;
+    e = ensure_smem<kernel>(kShared ? std::max(kShared, 48 * 1024 + 16) : 0);
+    return e == cudaSuccess ? launch_in_clusters(kernel, grid, 32 * W, 1, kShared, st, a, slabs) : e;
+  }
+  constexpr auto spans = scan_span_kernel<Act, SCALE, Span, false>;
+  cudaError_t e = ensure_smem<spans>(kRaised);
+  if (e == cudaSuccess) e = launch_in_clusters(spans, grid, 256, 1, kSpanShared, st, a, slabs);
+  if (e != cudaSuccess) return e;
+  using Eight = typename P::Eight;
+  constexpr int kShared = 8 * Eight::kBytes;
+  constexpr auto kernel = scan_kernel<Act, SCALE, Eight, 8, 1, 2, true>;
+  e = ensure_smem<kernel>(kShared ? std::max(kShared, 48 * 1024 + 16) : 0);
+  return e == cudaSuccess ? launch_in_clusters(kernel, grid, 256, 1, kShared, st, a, slabs) : e;
+}
+
 template <typename Act, int SCALE, class P>
 cudaError_t launch_scan_plan(const ScanArgs& a, bool backward, cudaStream_t st) {
   const int slabs = (a.C + kScanSlab - 1) / kScanSlab;
   const int64_t units = (int64_t)a.B * slabs;
+  if (a.spans) return launch_scan_split<Act, SCALE, P>(a, backward, slabs, st);
   if (backward) {
     // sequences of one run need no joins (52 x 2150 channels, 1 token: 35 us with a CTA each)
     if (a.L <= P::BackAlone::kTokens)

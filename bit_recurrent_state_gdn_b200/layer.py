@@ -128,38 +128,56 @@ class _Args:
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
         if need is not None:
+            n = 0
             if workspace is None:
                 n = need(cfg, self.shape[1])
+            if n:
                 on = None  # the current stream, which torch allocates for
                 if stream is not None:
                     on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
                 with torch.cuda.stream(on):
                     workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
-            self.on_device(workspace, "workspace")
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-            args += (workspace.data_ptr() or None, workspace.numel() * workspace.element_size())
+            if workspace is None:
+                args += (None, 0)
+            else:
+                self.on_device(workspace, "workspace")
+                if not workspace.is_contiguous():
+                    raise ValueError("workspace must be contiguous")
+                args += (workspace.data_ptr() or None,
+                         workspace.numel() * workspace.element_size())
         status = getattr(_abi.load(), where)(byref(cfg), self.shape[1], *args, handle)
         if status:
             raise GdnError(status, where)
 
 
-def gdn_gated_scan(cfg, x, g, o, h0=None, hT=None, hist=None, lens=None, stream=None):
+def gdn_gated_scan_workspace_bytes(cfg, L: int) -> int:
+    return int(_abi.load().gdn_gated_scan_workspace_bytes(byref(cfg), L))
+
+
+def _scan_workspace(cfg, L: int) -> int:
+    # a decode step does not pay for the question
+    return 0 if L < _abi.GDN_SCAN_SPLIT else gdn_gated_scan_workspace_bytes(cfg, L)
+
+
+def gdn_gated_scan(cfg, x, g, o, h0=None, hT=None, hist=None, lens=None, workspace=None,
+                   stream=None):
     """x, o act [B][L][H][D]; g fp32 [B][L][H][D], the log of the gate; h0, hT fp32 [B][H][D];
-    hist fp32 of gdn_scan_hist_shape(cfg, L), for the backward pass; lens int32 [B]."""
+    hist fp32 of gdn_scan_hist_shape(cfg, L), for the backward pass; lens int32 [B]. workspace: at
+    least gdn_gated_scan_workspace_bytes(cfg, L) bytes on the device, made here when None."""
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
     n = cfg.B * cfg.H * cfg.D
     f32, L = torch.float32, a.shape[1]
     a.call("gdn_gated_scan", cfg, (
         a.tokens(x, "x", act), a.tokens(g, "g", f32), a.tokens(o, "o", act),
         a.dense(h0, "h0", f32, n), a.dense(hT, "hT", f32, n),
-        a.dense(hist, "hist", f32, n * -(-L // _abi.GDN_SCAN_CHUNK)), a.lens(lens)), stream)
+        a.dense(hist, "hist", f32, n * -(-L // _abi.GDN_SCAN_CHUNK)), a.lens(lens)), stream,
+        workspace, _scan_workspace)
 
 
 def gdn_gated_scan_backward(cfg, x, g, hist, do, dx, dg, dhT=None, dh0=None, lens=None,
-                            stream=None):
+                            workspace=None, stream=None):
     """x, g, lens of the forward call and the hist that it wrote; do, dx act [B][L][H][D]; dg fp32
-    [B][L][H][D]; dhT, dh0 fp32 [B][H][D]."""
+    [B][L][H][D]; dhT, dh0 fp32 [B][H][D]; workspace as in the forward call."""
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
     n = cfg.B * cfg.H * cfg.D
     f32, L = torch.float32, a.shape[1]
@@ -167,7 +185,7 @@ def gdn_gated_scan_backward(cfg, x, g, hist, do, dx, dg, dhT=None, dh0=None, len
         a.tokens(x, "x", act), a.tokens(g, "g", f32),
         a.dense(hist, "hist", f32, n * -(-L // _abi.GDN_SCAN_CHUNK)), a.tokens(do, "do", act),
         a.dense(dhT, "dhT", f32, n), a.tokens(dx, "dx", act), a.tokens(dg, "dg", f32),
-        a.dense(dh0, "dh0", f32, n), a.lens(lens)), stream)
+        a.dense(dh0, "dh0", f32, n), a.lens(lens)), stream, workspace, _scan_workspace)
 
 
 def _norm_params(cfg) -> int:

@@ -59,6 +59,9 @@ typedef struct {
 /* Tokens between the states that gdn_gated_scan keeps for its backward pass. */
 #define GDN_SCAN_CHUNK 64
 
+/* Shorter sequences are never split: gdn_gated_scan and its backward need no workspace for them. */
+#define GDN_SCAN_SPLIT 4096
+
 /*
  * L tokens of the gated linear recurrence of every (sequence, head, channel), whose state is one
  * number (the matrix state of gdnq.h without keys and queries):
@@ -73,11 +76,20 @@ typedef struct {
  *   hist  fp32 [B][ceil(L / GDN_SCAN_CHUNK)][H][D], or NULL: the state before every 64th token,
  *         for gdn_gated_scan_backward. Chunks that begin at or behind a sequence's end are not
  *         written.
+ *   workspace  16-byte aligned, at least gdn_gated_scan_workspace_bytes(cfg, L) bytes (may be NULL
+ *         where that is 0): few and long sequences are split, and their parts' effects on the
+ *         state kept there. Contents are ignored on entry; calls whose work may overlap in time
+ *         need workspaces of their own.
  * L = 1 is the decode step.
  */
 gdn_status gdn_gated_scan(const gdn_scan_config* cfg, int32_t L, const gdn_tokens* x,
                           const gdn_tokens* g, const gdn_tokens* o, const float* h0, float* hT,
-                          float* hist, const int32_t* lens, gdn_stream_t stream);
+                          float* hist, const int32_t* lens, void* workspace,
+                          size_t workspace_bytes, gdn_stream_t stream);
+
+/* Bytes of workspace that gdn_gated_scan and gdn_gated_scan_backward need (0 for most sizes, and for
+ * a cfg that they reject). Host-only. */
+size_t gdn_gated_scan_workspace_bytes(const gdn_scan_config* cfg, int32_t L);
 
 /*
  * Gradients of gdn_gated_scan, from grad_o (the gradient of o) and grad_hT (that of hT, or NULL:
@@ -86,14 +98,15 @@ gdn_status gdn_gated_scan(const gdn_scan_config* cfg, int32_t L, const gdn_token
  *     grad_x_t = s(g_t) dh_t,   grad_g_t = a_t h_{t-1} dh_t + s'(g_t) x_t dh_t,
  *     grad_h0 = a_1 dh_1   (grad_hT for a sequence of no tokens).
  * s'(0) of GDN_SCALE_SQRT, where the root has no derivative, is taken as 0.
- *   x, g, lens as in the forward call; hist what that call wrote.
+ *   x, g, lens, workspace as in the forward call; hist what that call wrote.
  *   grad_x act tokens, grad_g fp32 tokens, grad_h0 fp32 [B][H][D] or NULL: written.
  */
 gdn_status gdn_gated_scan_backward(const gdn_scan_config* cfg, int32_t L, const gdn_tokens* x,
                                    const gdn_tokens* g, const float* hist,
                                    const gdn_tokens* grad_o, const float* grad_hT,
                                    const gdn_tokens* grad_x, const gdn_tokens* grad_g,
-                                   float* grad_h0, const int32_t* lens, gdn_stream_t stream);
+                                   float* grad_h0, const int32_t* lens, void* workspace,
+                                   size_t workspace_bytes, gdn_stream_t stream);
 
 /* ---- group norm --------------------------------------------------------------------------- */
 

@@ -98,6 +98,11 @@ SCAN = [
     (52, 1, 5, 43, "bf16", "complement", "wide", [1, 0, 1, 1] * 13),
     (33, 8, 2, 64, "bf16", "sqrt", "heads", None),
     (33, 5, 3, 33, "f32", "sqrt", "odd", [5, 0, 3] * 11),
+    # sequences split into spans
+    (1, 4096, 1, 16, "bf16", "sqrt", "tokens", None),
+    (3, 4500, 1, 70, "f32", "complement", "heads", [4500, 1, 4097]),
+    (2, 5001, 1, 33, "bf16", "none", "odd", [0, 4999]),
+    (5, 4200, 2, 64, "bf16", "sqrt", "wide", [4200, 129, 128, 2000, 4199]),
 ]
 
 
@@ -175,6 +180,19 @@ def test_scan_state_in_place_and_split_over_calls():
     for lo, hi in ((0, 100), (100, 101), (101, 161)):
         gdn.gdn_gated_scan(cfg, xs[:, lo:hi], gs[:, lo:hi], o[:, lo:hi], h0=h, hT=h)
     want, end, _, err, _, err_end = ref.scan(x, g, h0, "complement")
+    close(o, want, err, torch.float32)
+    close(h, end, err_end, torch.float32)
+
+
+def test_scan_state_in_place_of_split_sequences():
+    """Long sequences are split over CTAs that all need the first state, which the last one replaces."""
+    B, L, H, D = 2, 9000, 1, 96
+    x, g, h0, _ = scan_inputs(B, L, H, D, "f32", None, seed=6)
+    cfg = gdn.make_scan_config(B, H, D, scale="sqrt", act="f32")
+    assert gdn.gdn_gated_scan_workspace_bytes(cfg, L) > 0
+    h, o = h0.cuda(), torch.zeros_like(x, device="cuda")
+    gdn.gdn_gated_scan(cfg, x.cuda(), g.cuda(), o, h0=h, hT=h)
+    want, end, _, err, _, err_end = ref.scan(x, g, h0, "sqrt")
     close(o, want, err, torch.float32)
     close(h, end, err_end, torch.float32)
 

@@ -25,7 +25,7 @@ def tok(ptr=4096, sb=1 << 20, sl=64, sh=16):
 
 def scan_call(lib, cfg, L=4, x=None, g=None, o=None, lens=None):
     return lib.gdn_gated_scan(ctypes.byref(cfg), L, x or tok(4096), g or tok(8192), o or tok(12288),
-                              None, None, None, lens, None)
+                              None, None, None, lens, None, 0, None)
 
 
 def norm_call(lib, cfg, L=4, x=None, y=None, w=4096, z=None):
@@ -62,7 +62,7 @@ def test_sizes_beyond_the_limits_are_refused(lib, op):
     assert call(lib, make(B=1 << 20, H=1 << 10, D=128)) == BAD  # B H D > 2^36
     assert call(lib, make(), L=-1) == BAD
     assert call(lib, make(), L=(1 << 30) + 1) == BAD
-    assert lib.gdn_gated_scan(None, 1, *[None] * 8) == BAD
+    assert lib.gdn_gated_scan(None, 1, *[None] * 8, 0, None) == BAD
     assert lib.gdn_group_norm(None, 1, *[None] * 7) == BAD
     assert lib.gdn_short_conv(None, 1, *[None] * 8) == BAD
 
@@ -124,7 +124,7 @@ def test_backward_refusals(lib):
 
     def scan(hist=4096, dx=None, dg=None):
         return lib.gdn_gated_scan_backward(c(sc), 4, tok(4096), tok(8192), hist, tok(16384), None,
-                                           dx or tok(20480), dg or tok(24576), None, None, None)
+                                           dx or tok(20480), dg or tok(24576), None, None, None, 0, None)
 
     assert scan(hist=None) == BAD
     assert scan(dx=tok(4096)) == BAD and scan(dg=tok(8192)) == BAD
@@ -150,6 +150,16 @@ def test_backward_refusals(lib):
     need = gdn.gdn_short_conv_backward_workspace_bytes(cc, 4)
     assert need > 0 and conv(n=need - 1) == BAD
     assert conv(si=4096, dsi=4096) == BAD and conv(dso=4096, dsi=4096) == BAD
+
+
+def test_scan_workspace(lib):
+    """Only few and long sequences are split; a call that needs the workspace refuses to go without."""
+    long = MAKE["scan"][0](B=1, H=2)
+    need = gdn.gdn_gated_scan_workspace_bytes(long, 5000)
+    assert need > 0 and gdn.gdn_gated_scan_workspace_bytes(long, 4095) == 0
+    assert gdn.gdn_gated_scan_workspace_bytes(MAKE["scan"][0](B=40), 5000) == 0
+    assert gdn.gdn_gated_scan_workspace_bytes(gdn.make_scan_config(0, 2, 16), 5000) == 0
+    assert scan_call(lib, long, L=5000) == BAD and b"workspace" in lib.gdn_last_error()
 
 
 def test_workspaces_of_what_is_refused_are_empty(lib):
