@@ -18,7 +18,7 @@ size_t scan_spans(ScanArgs& a) {
   const int64_t want = (2 * kSms) / units, tokens = (a.L + want - 1) / want;
   a.span_tokens = (int)((tokens + kGrain - 1) / kGrain * kGrain);
   a.spans_per_unit = (a.L + a.span_tokens - 1) / a.span_tokens;
-  return (size_t)units * (size_t)(a.spans_per_unit + 1) * 32 * sizeof(Link);
+  return (size_t)units * (size_t)(a.spans_per_unit + 1) * 32 * (sizeof(SpanLink) + sizeof(SpanDecay));
 }
 
 }  // namespace gdnq

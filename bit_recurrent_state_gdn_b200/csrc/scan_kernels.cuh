@@ -1,16 +1,17 @@
 // Gated scan h_t = a_t h_{t-1} + s(g_t) x_t, a_t = e^{g_t}, and its gradients
 // (include/gdnq_layer.h).
 //
-// Mathematics. A run of tokens acts on the state as h -> A h + B, with A = e^{sum g} and B its
-// scan from zero, so that runs can be scanned side by side and joined: A is formed from the sum
-// of the gates, one rounding however long the run. The gradient runs from the last token to the
-// first in the same way: with c the gradient that reaches a token's state from behind,
-// dh = grad_o + c, and c <- a dh, a run acts as c -> A c + R with the same A.
+// Mathematics. A run of up to 16 tokens acts on the state as h -> A h + B, with A = e^{sum g} and B
+// its scan from zero, so that runs can be scanned side by side and joined: A is formed from the sum
+// of the gates, one rounding for the run, and is a product over several runs. The gradient runs from
+// the last token to the first in the same way: with c the gradient that reaches a token's state from
+// behind, dh = grad_o + c, and c <- a dh, a run acts as c -> A c + R with the same A.
 //
 // Split. A warp takes 64 channels and T consecutive tokens at a time in registers; W warps
 // of a CTA (a group) and CL CTAs of a cluster take the runs that follow one another, join them
 // through shared memory, and walk the sequence together, the next tile's loads under way while
-// the present one is scanned. Each array is read and written once.
+// the present one is scanned. Each array is read and written once, but for few and long sequences,
+// whose spans' effects are found by a pass of their own (see SpanLink).
 #pragma once
 
 #include "layer_util.cuh"
@@ -377,32 +378,132 @@ constexpr int scan_threads(int W) { return 32 * W * scan_groups(W); }
 // A first kernel leaves what every span does to the state; a span's state is then what the spans
 // before it (backward, behind it) make of the sequence's. It reads a part of the data twice, where
 // one chain of clusters would leave most of the machine idle.
-// Link 0 of a unit is its first state (forward), link i + 1 span i's.
-__device__ __forceinline__ Link* span_links(const ScanArgs& a, int64_t units, int64_t unit, int link) {
-  return static_cast<Link*>(a.spans) + (link * units + unit) * 32 + (threadIdx.x & 31);
+//
+// The decay of a span, or of many, need not be a number where no state ever meets it: gates a little
+// above 1 over a state of zero. So it is also kept with an exponent of its own, a 2^e with 1 <= a < 2
+// (or a is 0, infinite or NaN). Below 2^-300 it takes every fp32 state to zero and is zero, above
+// 2^300 it takes every other state beyond fp32 and is 2^300. To join spans by such decays is bound by
+// their instructions (64 channels x 131072 tokens, 256 spans: 37 us, 33 with plain numbers), so that is
+// for sequences with a gate above 1; elsewhere no product of decays is above 1 either.
+struct alignas(16) SpanDecay {
+  F2 a;
+  int e[2];
+};
+// What a span does: h -> p h + b, with p = a 2^e, or 2 where the span has a gate above 1: then the
+// decay is to be taken from there.
+struct alignas(16) SpanLink {
+  F2 b, p;
+};
+
+// Takes the exponent of a (normal, 0, infinite or NaN) into e, which is 0 with a decay of zero.
+__device__ __forceinline__ float scaled(float a, int& e) {
+  const uint32_t bits = __float_as_uint(a), field = bits >> 23 & 255;
+  const int shift = field == 255 ? 0 : (int)field - 127;
+  e = min(e + shift, 300);
+  const bool zero = field == 0 || e < -300;
+  e = zero ? 0 : e;
+  return zero ? 0.0f : __uint_as_float(bits - ((uint32_t)shift << 23));
 }
 
-__device__ __forceinline__ Link join(const Link& first, const Link& then) {
-  return Link{f2_mul(then.a, first.a), f2_fma(then.a, first.b, then.b)};
+__device__ __forceinline__ F2 scaled(F2 a, int (&e)[2]) {
+  float lo, hi;
+  f2_get(a, lo, hi);
+  lo = scaled(lo, e[0]);
+  hi = scaled(hi, e[1]);
+  return f2(lo, hi);
 }
 
-// The links from `from` on, `count` of them in steps of `step`, joined in that order: an equal part
-// by each of the CTA's W warps, the parts in shared memory. The same in every warp.
+// The part of 2^e within [2^-100, 2^100]; the rest of e stays.
+__device__ __forceinline__ float take_power(int& e) {
+  const int part = max(-100, min(e, 100));
+  e -= part;
+  return __uint_as_float((uint32_t)(part + 127) << 23);
+}
+
+__device__ __forceinline__ F2 take_power(int (&e)[2]) {
+  const float lo = take_power(e[0]), hi = take_power(e[1]);
+  return f2(lo, hi);
+}
+
+// The factors of a 2^e, e within +-300, one after the other.
+__device__ __forceinline__ void factors(const SpanDecay& d, F2 (&f)[3]) {
+  int e[2] = {d.e[0], d.e[1]};
+  f[0] = f2_mul(take_power(e), d.a);
+  f[1] = take_power(e);
+  f[2] = take_power(e);
+}
+
+__device__ __forceinline__ F2 decayed(const F2 (&f)[3], F2 h, F2 b) {
+  return f2_fma(f2_mul(f2_mul(h, f[0]), f[1]), f[2], b);
+}
+
+__device__ __forceinline__ bool above(F2 f, float limit) {
+  float lo, hi;
+  f2_get(f, lo, hi);
+  return lo > limit || hi > limit;
+}
+
+// The workspace: links [link][unit][32], link 0 of a unit its first state (forward), link i + 1 span
+// i's; behind them the spans' decays in the same order.
+__device__ __forceinline__ SpanLink* span_links(const ScanArgs& a, int64_t units, int64_t unit, int link) {
+  return static_cast<SpanLink*>(a.spans) + (link * units + unit) * 32 + (threadIdx.x & 31);
+}
+
+__device__ __forceinline__ SpanDecay* span_decays(const ScanArgs& a, int64_t units, int64_t unit, int link) {
+  return reinterpret_cast<SpanDecay*>(span_links(a, units, unit, a.spans_per_unit + 1 + link));
+}
+
+// A warp's part of a sequence: its b and the factors of its decay, [4][W][32] in shared memory.
 template <int W>
-__device__ __forceinline__ Link join_spans(const ScanArgs& a, int64_t units, int64_t unit, int from,
-                                           int count, int step, Link (*shared)[32]) {
+struct SpanPart {
+  static __device__ __forceinline__ void put(F2* shared, F2 b, const F2 (&f)[3]) {
+    shared[threadIdx.x] = b;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) shared[(k + 1) * W * 32 + threadIdx.x] = f[k];
+  }
+  static __device__ __forceinline__ F2 apply(const F2* shared, int w, F2 h) {
+    const F2* at = shared + w * 32 + (threadIdx.x & 31);
+    const F2 f[3] = {at[W * 32], at[2 * W * 32], at[3 * W * 32]};
+    return decayed(f, h, at[0]);
+  }
+};
+
+// What the links from `from` on, `count` of them in steps of `step`, make of the state: an equal part
+// of them joined by each of the CTA's W warps, the parts in shared memory. The same in every warp.
+template <int W>
+__device__ __forceinline__ F2 join_spans(const ScanArgs& a, int64_t units, int64_t unit, F2 state,
+                                         int from, int count, int step, F2* shared) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int share = (count + W - 1) / W, begin = w * share, end = min(begin + share, count);
-  Link all = {f2_all(1.0f), f2_all(0.0f)};
+  SpanLink all = {f2_all(0.0f), f2_all(1.0f)};
+  bool grows = false;
 #pragma unroll 8
-  for (int i = begin; i < end; ++i) all = join(all, *span_links(a, units, unit, from + i * step));
-  shared[w][lane] = all;
+  for (int i = begin; i < end; ++i) {
+    const SpanLink l = *span_links(a, units, unit, from + i * step);
+    grows = grows || above(l.p, 1.0f);
+    all.b = f2_fma(l.p, all.b, l.b);
+    all.p = f2_mul(l.p, all.p);
+  }
+  F2 f[3] = {all.p, f2_all(1.0f), f2_all(1.0f)};
+  if (__syncthreads_or(grows)) {
+    SpanDecay d = {f2_all(1.0f), {0, 0}};
+    all.b = f2_all(0.0f);
+    for (int i = begin; i < end; ++i) {
+      const SpanDecay next = *span_decays(a, units, unit, from + i * step);
+      factors(next, f);
+      all.b = decayed(f, all.b, span_links(a, units, unit, from + i * step)->b);
+      d.e[0] += next.e[0];
+      d.e[1] += next.e[1];
+      d.a = scaled(f2_mul(next.a, d.a), d.e);
+    }
+    factors(d, f);
+  }
+  SpanPart<W>::put(shared, all.b, f);
   __syncthreads();
-  all = shared[0][lane];
 #pragma unroll
-  for (int i = 1; i < W; ++i) all = join(all, shared[i][lane]);
+  for (int i = 0; i < W; ++i) state = SpanPart<W>::apply(shared, i, state);
   __syncthreads();
-  return all;
+  return state;
 }
 
 // A warp takes an eighth of a span. Backward `in` is grad_o, and a run acts on the gradient that
@@ -411,7 +512,8 @@ template <typename Act, int SCALE, class Runs, bool BACKWARD>
 __global__ void __launch_bounds__(256, 2) scan_span_kernel(ScanArgs a, int slabs) {
   constexpr int W = 8, T = Runs::kTokens;
   extern __shared__ __align__(128) uint8_t rings[];
-  __shared__ alignas(16) Link part[W][32];
+  __shared__ F2 part[4 * W * 32];
+  __shared__ SpanDecay decay[W][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t units = (int64_t)a.B * slabs, unit = blockIdx.x % units;
   const int span = (int)(blockIdx.x / units);
@@ -421,15 +523,17 @@ __global__ void __launch_bounds__(256, 2) scan_span_kernel(ScanArgs a, int slabs
     // the state before the sequence: the second kernel's CTAs read it here, since hT may be h0
     const ScanLane me = scan_lane<Runs::kStep>(a, slab);
     const int64_t state = (int64_t)b * a.C + me.c;
-    *span_links(a, units, unit, 0) = Link{
-        f2_all(0.0f), a.h0 && me.live ? state_load<Runs::kStep>(a.h0 + state, me.both) : f2_all(0.0f)};
+    span_links(a, units, unit, 0)->b =
+        a.h0 && me.live ? state_load<Runs::kStep>(a.h0 + state, me.both) : f2_all(0.0f);
   }
   if (first >= len) return;
   const int share = a.span_tokens / W, begin = first + w * share, end = min(begin + share, len);
   Runs runs(a, rings + w * Runs::kBytes, b, slab, end);
   const int tiles = end > begin ? (end - begin + T - 1) / T : 0;
   runs.start(BACKWARD ? begin + (tiles - 1) * T : begin, BACKWARD ? -T : T);
-  Link all = {f2_all(1.0f), f2_all(0.0f)};
+  F2 state = f2_all(0.0f);
+  SpanDecay all = {f2_all(1.0f), {0, 0}};
+  float most = 0.0f;  // of the gates' logs
   for (int tile = 0; tile < tiles; ++tile) {
     runs.take();
     F2 g_sum = f2_all(0.0f), at[T];
@@ -437,26 +541,52 @@ __global__ void __launch_bounds__(256, 2) scan_span_kernel(ScanArgs a, int slabs
     for (int j = 0; j < T; ++j) {
       const F2 gj = runs.g(j);
       const Gate q = gate_of<BACKWARD ? GDN_SCALE_NONE : SCALE>(gj);
+      float g0, g1;
+      f2_get(gj, g0, g1);
+      most = fmaxf(most, fmaxf(g0, g1));
       at[j] = q.a;
       g_sum = f2_add(g_sum, gj);
-      if constexpr (!BACKWARD) all.b = f2_fma(q.a, all.b, f2_mul(q.s, runs.x(j)));
+      if constexpr (!BACKWARD) state = f2_fma(q.a, state, f2_mul(q.s, runs.x(j)));
     }
     if constexpr (BACKWARD) {
 #pragma unroll
-      for (int j = T - 1; j >= 0; --j) all.b = f2_mul(at[j], f2_add(runs.x(j), all.b));
+      for (int j = T - 1; j >= 0; --j) state = f2_mul(at[j], f2_add(runs.x(j), state));
     }
     all.a = f2_mul(all.a, run_decay(g_sum));
+    // 128 tokens multiply by less than e^88 < 2^127
+    if (tile % (128 / T) == 128 / T - 1) all.a = scaled(all.a, all.e);
     runs.next();
   }
   runs.finish();
-  part[w][lane] = all;
-  __syncthreads();
+  all.a = scaled(all.a, all.e);
+  F2 f[3];
+  factors(all, f);
+  SpanPart<W>::put(part, state, f);
+  decay[w][lane] = all;
+  const bool grows = __syncthreads_or(most > 0.0f);
   if (w == 0) {
-    all = part[BACKWARD ? W - 1 : 0][lane];
+    state = f2_all(0.0f);
 #pragma unroll
-    for (int i = 1; i < W; ++i) all = join(all, part[BACKWARD ? W - 1 - i : i][lane]);
-    *span_links(a, units, unit, span + 1) = all;
+    for (int i = 0; i < W; ++i) state = SpanPart<W>::apply(part, BACKWARD ? W - 1 - i : i, state);
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      all.a = f2_mul(all.a, decay[i][lane].a);  // of eight numbers below 2
+      all.e[0] += decay[i][lane].e[0];
+      all.e[1] += decay[i][lane].e[1];
+    }
+    all.a = scaled(all.a, all.e);
+    factors(all, f);
+    *span_links(a, units, unit, span + 1) =
+        SpanLink{state, grows ? f2_all(2.0f) : decayed(f, f2_all(1.0f), f2_all(0.0f))};
+    *span_decays(a, units, unit, span + 1) = all;
   }
+}
+
+// The joins' two buffers of links, which hold the W parts of a sequence before the first tile.
+template <int W>
+__device__ __forceinline__ F2* parts_of(Link (&agg)[2][W][32]) {
+  static_assert(sizeof(agg) == 4 * W * 32 * sizeof(F2), "as large");
+  return &agg[0][0][0].a;
 }
 
 template <typename Act, int SCALE, class Runs, int W, int CL, int MINB, bool SPLIT = false>
@@ -490,7 +620,7 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_kernel(ScanArgs a,
                     : nullptr;
   F2 carry;  // before the tile
   if constexpr (SPLIT)
-    carry = join_spans<W>(a, units, unit, 0, span + 1, 1, agg[0]).b;
+    carry = join_spans<W>(a, units, unit, span_links(a, units, unit, 0)->b, 1, span, 1, parts_of(agg));
   else
     carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);
 
@@ -603,8 +733,7 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_backward_kernel(Sc
 
   if constexpr (SPLIT) {
     const int last = (length + a.span_tokens - 1) / a.span_tokens;  // the last span's link
-    const Link l = join_spans<W>(a, units, unit, last, max(last - span - 1, 0), -1, agg[0]);
-    carry = f2_fma(l.a, carry, l.b);
+    carry = join_spans<W>(a, units, unit, carry, last, max(last - span - 1, 0), -1, parts_of(agg));
   }
 
   // the kept state before the CTA's tile that begins at `first`

@@ -67,9 +67,10 @@ typedef struct {
  * number (the matrix state of gdnq.h without keys and queries):
  *     h_t = a_t h_{t-1} + s(g_t) x_t,   a_t = e^{g_t},   o_t = h_t.
  * g_t = -inf forgets all before (the first token of a document in a packed row); g_t = 0 with
- * x_t = 0 changes nothing. Runs of tokens are joined by the exponential of their summed gates: a
- * gate above 1 (g_t > 0, not with GDN_SCALE_SQRT) is taken too, as long as no 1024 tokens' gates
- * sum to 88 or more. Gates below 2^-126 count as zero.
+ * x_t = 0 changes nothing. Runs of tokens are joined by the products of their gates: a gate above 1
+ * (g_t > 0, not with GDN_SCALE_SQRT) is taken too, as long as in no stretch of up to 1024 tokens the
+ * gates' logs sum to 88 or more. A gate, or a product of successive tokens' gates, below 2^-126 may
+ * count as zero.
  *   x     act tokens;  g  fp32 tokens, the log of the gate;  o  act tokens, written.
  *   h0    fp32 [B][H][D], the states before the first token, or NULL: zero.
  *   hT    fp32 [B][H][D], the states after each sequence's last token, or NULL; may be h0.
