@@ -443,8 +443,8 @@ __device__ __forceinline__ bool above(F2 f, float limit) {
   return lo > limit || hi > limit;
 }
 
-// The workspace: links [link][unit][32], link 0 of a unit its first state (forward), link i + 1 span
-// i's; behind them the spans' decays in the same order.
+// The workspace: links [link][unit][32], link 0 of a unit its first state (backward the gradient of
+// its last one), link i + 1 span i's; behind them the spans' decays in the same order.
 __device__ __forceinline__ SpanLink* span_links(const ScanArgs& a, int64_t units, int64_t unit, int link) {
   return static_cast<SpanLink*>(a.spans) + (link * units + unit) * 32 + (threadIdx.x & 31);
 }
@@ -519,8 +519,9 @@ __global__ void __launch_bounds__(256, 2) scan_span_kernel(ScanArgs a, int slabs
   const int span = (int)(blockIdx.x / units);
   const int b = (int)(unit / slabs), slab = (int)(unit % slabs);
   const int len = seq_len(a.lens, b, a.L), first = span * a.span_tokens;
-  if (!BACKWARD && span == 0 && w == 0) {
-    // the state before the sequence: the second kernel's CTAs read it here, since hT may be h0
+  if (span == 0 && w == 0) {
+    // the state before the sequence (the gradient behind it): the second kernel's CTAs read it here,
+    // since hT may be h0 (grad_h0 grad_hT)
     const ScanLane me = scan_lane<Runs::kStep>(a, slab);
     const int64_t state = (int64_t)b * a.C + me.c;
     span_links(a, units, unit, 0)->b =
@@ -729,11 +730,13 @@ __global__ void __launch_bounds__(scan_threads(W), MINB) scan_backward_kernel(Sc
   const float* hist =
       a.hist + (int64_t)b * ((a.L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK) * a.C + me.c;
   // the gradient that reaches the tile's last state from behind
-  F2 carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);
-
+  F2 carry;
   if constexpr (SPLIT) {
     const int last = (length + a.span_tokens - 1) / a.span_tokens;  // the last span's link
-    carry = join_spans<W>(a, units, unit, carry, last, max(last - span - 1, 0), -1, parts_of(agg));
+    carry = join_spans<W>(a, units, unit, span_links(a, units, unit, 0)->b, last, max(last - span - 1, 0),
+                          -1, parts_of(agg));
+  } else {
+    carry = a.h0 && live ? state_load<STEP>(a.h0 + state, me.both) : f2_all(0.0f);
   }
 
   // the kept state before the CTA's tile that begins at `first`

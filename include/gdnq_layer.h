@@ -100,7 +100,7 @@ size_t gdn_gated_scan_workspace_bytes(const gdn_scan_config* cfg, int32_t L);
  *     grad_h0 = a_1 dh_1   (grad_hT for a sequence of no tokens).
  * s'(0) of GDN_SCALE_SQRT, where the root has no derivative, is taken as 0.
  *   x, g, lens, workspace as in the forward call; hist what that call wrote.
- *   grad_x act tokens, grad_g fp32 tokens, grad_h0 fp32 [B][H][D] or NULL: written.
+ *   grad_x act tokens, grad_g fp32 tokens, grad_h0 fp32 [B][H][D] or NULL (may be grad_hT): written.
  */
 gdn_status gdn_gated_scan_backward(const gdn_scan_config* cfg, int32_t L, const gdn_tokens* x,
                                    const gdn_tokens* g, const float* hist,
