@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "layer_args.h"
+#include "overlap.h"
 #include "status.h"
 
 using gdnq::clear_error;
@@ -17,6 +18,7 @@ namespace {
 struct Shape {
   int64_t B, L, H, D;
   bool empty() const { return B == 0 || H == 0; }
+  size_t heads() const { return (size_t)B * (size_t)H * (size_t)D; }  // elements of [B][H][D]
 };
 
 gdn_status check_shape(int64_t B, int64_t L, int64_t H, int64_t D, int act_dtype) {
@@ -69,13 +71,6 @@ gdn_status check_opt(const void* p, const char* name, unsigned align) {
   return p ? need_ptr(p, name, align) : GDN_OK;
 }
 
-// An output array that begins where another array does.
-gdn_status check_apart(const void* out, const void* other, const char* a, const char* b) {
-  if (out && out == other)
-    return fail(GDN_ERR_INVALID_ARG, "%s may not be %s", a, b);
-  return GDN_OK;
-}
-
 gdn_status check_workspace(const void* ws, size_t have, size_t need) {
   if (need == 0) return GDN_OK;
   gdn_status st = need_ptr(ws, "workspace");
@@ -83,6 +78,17 @@ gdn_status check_workspace(const void* ws, size_t have, size_t need) {
   if (have < need)
     return fail(GDN_ERR_INVALID_ARG, "workspace holds %zu bytes, the call needs %zu", have, need);
   return GDN_OK;
+}
+
+void add(gdnq::Arrays& all, const gdn_tokens* t, const char* name, const Shape& s, unsigned elem,
+         bool output) {
+  all.tokens(t, name, s.B, s.L, s.H, s.D, elem, output);
+}
+
+int64_t chunks(int64_t L) { return (L + GDN_SCAN_CHUNK - 1) / GDN_SCAN_CHUNK; }
+
+size_t norm_params(const gdn_norm_config* c) {
+  return (size_t)c->D * (c->weight == GDN_WEIGHT_CHANNEL ? (size_t)c->H : 1);
 }
 
 gdnq::Tok tok(const gdn_tokens* t) {
@@ -201,10 +207,6 @@ gdn_status gdn_gated_scan(const gdn_scan_config* cfg, int32_t L, const gdn_token
   GDNQ_TRY(check_tokens(x, "x", s, e, false));
   GDNQ_TRY(check_tokens(g, "g", s, 4, false));
   GDNQ_TRY(check_tokens(o, "o", s, e, true));
-  if (L > 0) {
-    GDNQ_TRY(check_apart(o->ptr, x->ptr, "o", "x"));
-    GDNQ_TRY(check_apart(o->ptr, g->ptr, "o", "g"));
-  }
   GDNQ_TRY(check_opt(h0, "h0", 4));
   GDNQ_TRY(check_opt(hT, "hT", 4));
   GDNQ_TRY(check_opt(hist, "hist", 4));
@@ -215,6 +217,13 @@ gdn_status gdn_gated_scan(const gdn_scan_config* cfg, int32_t L, const gdn_token
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D;
   const size_t need = gdnq::scan_spans(a);
   GDNQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  gdnq::Arrays all;
+  add(all, x, "x", s, e, false), add(all, g, "g", s, 4, false), add(all, o, "o", s, e, true);
+  const size_t state = 4 * s.heads();
+  all.dense(h0, "h0", state, false), all.dense(hT, "hT", state, true);
+  all.dense(hist, "hist", state * (size_t)chunks(L), true);
+  all.dense(lens, "lens", 4 * (size_t)s.B, false), all.dense(workspace, "workspace", need, true);
+  GDNQ_TRY(all.check(hT, h0));
   a.spans = need > 0 ? workspace : nullptr;
   const cudaError_t err = launch_scan(a, cfg, false, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_gated_scan");
@@ -236,18 +245,7 @@ gdn_status gdn_gated_scan_backward(const gdn_scan_config* cfg, int32_t L, const 
   GDNQ_TRY(check_tokens(grad_o, "grad_o", s, e, false));
   GDNQ_TRY(check_tokens(grad_x, "grad_x", s, e, true));
   GDNQ_TRY(check_tokens(grad_g, "grad_g", s, 4, true));
-  if (L > 0) {
-    GDNQ_TRY(need_ptr(hist, "hist", 4));
-    const struct {
-      const gdn_tokens* t;
-      const char* name;
-    } in[3] = {{x, "x"}, {g, "g"}, {grad_o, "grad_o"}};
-    for (const auto& i : in) {
-      GDNQ_TRY(check_apart(grad_x->ptr, i.t->ptr, "grad_x", i.name));
-      GDNQ_TRY(check_apart(grad_g->ptr, i.t->ptr, "grad_g", i.name));
-    }
-    GDNQ_TRY(check_apart(grad_g->ptr, grad_x->ptr, "grad_g", "grad_x"));
-  }
+  if (L > 0) GDNQ_TRY(need_ptr(hist, "hist", 4));
   GDNQ_TRY(check_opt(grad_hT, "grad_hT", 4));
   GDNQ_TRY(check_opt(grad_h0, "grad_h0", 4));
   GDNQ_TRY(check_opt(lens, "lens", 4));
@@ -258,6 +256,14 @@ gdn_status gdn_gated_scan_backward(const gdn_scan_config* cfg, int32_t L, const 
   a.B = cfg->B, a.L = L, a.H = cfg->H, a.D = cfg->D, a.C = cfg->H * cfg->D;
   const size_t need = gdnq::scan_spans(a);
   GDNQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  gdnq::Arrays all;
+  add(all, x, "x", s, e, false), add(all, g, "g", s, 4, false), add(all, grad_o, "grad_o", s, e, false);
+  add(all, grad_x, "grad_x", s, e, true), add(all, grad_g, "grad_g", s, 4, true);
+  const size_t state = 4 * s.heads();
+  all.dense(grad_hT, "grad_hT", state, false), all.dense(grad_h0, "grad_h0", state, true);
+  all.dense(hist, "hist", state * (size_t)chunks(L), false);
+  all.dense(lens, "lens", 4 * (size_t)s.B, false), all.dense(workspace, "workspace", need, true);
+  GDNQ_TRY(all.check(grad_h0, grad_hT));
   a.spans = need > 0 ? workspace : nullptr;
   const cudaError_t err = launch_scan(a, cfg, true, stream);
   return err == cudaSuccess ? GDN_OK : cuda_fail(err, "gdn_gated_scan_backward");
@@ -275,11 +281,15 @@ gdn_status gdn_group_norm(const gdn_norm_config* cfg, int32_t L, const gdn_token
   if (z) GDNQ_TRY(check_tokens(z, "z", s, e, false));
   GDNQ_TRY(check_tokens(y, "y", s, e, true));
   if (L == 0) return GDN_OK;
-  GDNQ_TRY(check_apart(y->ptr, x->ptr, "y", "x"));
-  if (z) GDNQ_TRY(check_apart(y->ptr, z->ptr, "y", "z"));
   GDNQ_TRY(need_ptr(w, "w", 4));
   GDNQ_TRY(check_opt(bias, "bias", 4));
   GDNQ_TRY(check_opt(lens, "lens", 4));
+  gdnq::Arrays all;
+  add(all, x, "x", s, e, false), add(all, z, "z", s, e, false), add(all, y, "y", s, e, true);
+  const size_t params = 4 * norm_params(cfg);
+  all.dense(w, "w", params, false), all.dense(bias, "bias", params, false);
+  all.dense(lens, "lens", 4 * (size_t)s.B, false);
+  GDNQ_TRY(all.check());
   gdnq::NormArgs a = norm_args(cfg, L);
   a.x = tok(x), a.z = tok(z), a.y = tok(y);
   a.w = w, a.bias = bias, a.lens = lens;
@@ -311,7 +321,7 @@ gdn_status gdn_group_norm_backward(const gdn_norm_config* cfg, int32_t L, const 
   GDNQ_TRY(need_ptr(grad_w, "grad_w", 4));
   GDNQ_TRY(check_opt(grad_bias, "grad_bias", 4));
   if (s.B == 0 || L == 0) {
-    const size_t n = (size_t)s.D * (cfg->weight == GDN_WEIGHT_CHANNEL ? (size_t)s.H : 1);
+    const size_t n = norm_params(cfg);
     GDNQ_TRY(zero(grad_w, n, stream, "gdn_group_norm_backward"));
     return zero(grad_bias, n, stream, "gdn_group_norm_backward");
   }
@@ -321,21 +331,18 @@ gdn_status gdn_group_norm_backward(const gdn_norm_config* cfg, int32_t L, const 
   GDNQ_TRY(check_tokens(grad_y, "grad_y", s, e, false));
   GDNQ_TRY(check_tokens(grad_x, "grad_x", s, e, true));
   if (z) GDNQ_TRY(check_tokens(grad_z, "grad_z", s, e, true));
-  const struct {
-    const gdn_tokens* t;
-    const char* name;
-  } in[3] = {{x, "x"}, {z, "z"}, {grad_y, "grad_y"}};
-  for (const auto& i : in) {
-    if (!i.t) continue;
-    GDNQ_TRY(check_apart(grad_x->ptr, i.t->ptr, "grad_x", i.name));
-    if (z) GDNQ_TRY(check_apart(grad_z->ptr, i.t->ptr, "grad_z", i.name));
-  }
-  if (z) GDNQ_TRY(check_apart(grad_z->ptr, grad_x->ptr, "grad_z", "grad_x"));
-  GDNQ_TRY(check_apart(grad_bias, grad_w, "grad_bias", "grad_w"));
   GDNQ_TRY(need_ptr(w, "w", 4));
   GDNQ_TRY(check_opt(bias, "bias", 4));
   GDNQ_TRY(check_opt(lens, "lens", 4));
-  GDNQ_TRY(check_workspace(workspace, workspace_bytes, gdnq::norm_backward_workspace(*cfg, L)));
+  const size_t need = gdnq::norm_backward_workspace(*cfg, L), params = 4 * norm_params(cfg);
+  GDNQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  gdnq::Arrays all;
+  add(all, x, "x", s, e, false), add(all, z, "z", s, e, false), add(all, grad_y, "grad_y", s, e, false);
+  add(all, grad_x, "grad_x", s, e, true), add(all, grad_z, "grad_z", s, e, true);
+  all.dense(w, "w", params, false), all.dense(bias, "bias", params, false);
+  all.dense(grad_w, "grad_w", params, true), all.dense(grad_bias, "grad_bias", params, true);
+  all.dense(lens, "lens", 4 * (size_t)s.B, false), all.dense(workspace, "workspace", need, true);
+  GDNQ_TRY(all.check());
   gdnq::NormArgs a = norm_args(cfg, L);
   a.x = tok(x), a.z = tok(z);
   a.grad_y = tok(grad_y), a.grad_x = tok(grad_x), a.grad_z = tok(grad_z);
@@ -356,12 +363,18 @@ gdn_status gdn_short_conv(const gdn_conv_config* cfg, int32_t L, const gdn_token
   const unsigned e = act_bytes(cfg->act_dtype);
   GDNQ_TRY(check_tokens(x, "x", s, e, false));
   GDNQ_TRY(check_tokens(y, "y", s, e, true));
-  if (L > 0) GDNQ_TRY(check_apart(y->ptr, x->ptr, "y", "x"));
   GDNQ_TRY(need_ptr(w, "w", 4));
   GDNQ_TRY(check_opt(bias, "bias", 4));
   GDNQ_TRY(check_opt(state_in, "state_in", e));
   GDNQ_TRY(check_opt(state_out, "state_out", e));
   GDNQ_TRY(check_opt(lens, "lens", 4));
+  gdnq::Arrays all;
+  add(all, x, "x", s, e, false), add(all, y, "y", s, e, true);
+  const size_t C = (size_t)(s.H * s.D), state = (size_t)e * s.heads() * (size_t)(cfg->K - 1);
+  all.dense(w, "w", 4 * C * (size_t)cfg->K, false), all.dense(bias, "bias", 4 * C, false);
+  all.dense(state_in, "state_in", state, false), all.dense(state_out, "state_out", state, true);
+  all.dense(lens, "lens", 4 * (size_t)s.B, false);
+  GDNQ_TRY(all.check(state_out, state_in));
   gdnq::ConvArgs a{};
   a.x = tok(x), a.y = tok(y);
   a.w = w, a.bias = bias, a.state_in = state_in, a.state_out = state_out, a.lens = lens;
@@ -392,7 +405,6 @@ gdn_status gdn_short_conv_backward(const gdn_conv_config* cfg, int32_t L, const 
     return fail(GDN_ERR_INVALID_ARG, "grad_bias goes with bias");
   GDNQ_TRY(need_ptr(grad_w, "grad_w", 4));
   GDNQ_TRY(check_opt(grad_bias, "grad_bias", 4));
-  GDNQ_TRY(check_apart(grad_bias, grad_w, "grad_bias", "grad_w"));
   if (s.B == 0) {
     const size_t n = (size_t)s.H * (size_t)s.D;
     GDNQ_TRY(zero(grad_w, n * (size_t)cfg->K, stream, "gdn_short_conv_backward"));
@@ -402,19 +414,24 @@ gdn_status gdn_short_conv_backward(const gdn_conv_config* cfg, int32_t L, const 
   GDNQ_TRY(check_tokens(x, "x", s, e, false));
   GDNQ_TRY(check_tokens(grad_y, "grad_y", s, e, false));
   GDNQ_TRY(check_tokens(grad_x, "grad_x", s, e, true));
-  if (L > 0) {
-    GDNQ_TRY(check_apart(grad_x->ptr, x->ptr, "grad_x", "x"));
-    GDNQ_TRY(check_apart(grad_x->ptr, grad_y->ptr, "grad_x", "grad_y"));
-  }
   GDNQ_TRY(need_ptr(w, "w", 4));
   GDNQ_TRY(check_opt(bias, "bias", 4));
   GDNQ_TRY(check_opt(state_in, "state_in", e));
   GDNQ_TRY(check_opt(grad_state_out, "grad_state_out", e));
   GDNQ_TRY(check_opt(grad_state_in, "grad_state_in", e));
-  GDNQ_TRY(check_apart(grad_state_in, state_in, "grad_state_in", "state_in"));
-  GDNQ_TRY(check_apart(grad_state_in, grad_state_out, "grad_state_in", "grad_state_out"));
   GDNQ_TRY(check_opt(lens, "lens", 4));
-  GDNQ_TRY(check_workspace(workspace, workspace_bytes, gdnq::conv_backward_workspace(*cfg, L)));
+  const size_t need = gdnq::conv_backward_workspace(*cfg, L);
+  GDNQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  gdnq::Arrays all;
+  add(all, x, "x", s, e, false), add(all, grad_y, "grad_y", s, e, false), add(all, grad_x, "grad_x", s, e, true);
+  const size_t C = (size_t)(s.H * s.D), state = (size_t)e * s.heads() * (size_t)(cfg->K - 1);
+  all.dense(w, "w", 4 * C * (size_t)cfg->K, false), all.dense(bias, "bias", 4 * C, false);
+  all.dense(grad_w, "grad_w", 4 * C * (size_t)cfg->K, true), all.dense(grad_bias, "grad_bias", 4 * C, true);
+  all.dense(state_in, "state_in", state, false);
+  all.dense(grad_state_out, "grad_state_out", state, false);
+  all.dense(grad_state_in, "grad_state_in", state, true);
+  all.dense(lens, "lens", 4 * (size_t)s.B, false), all.dense(workspace, "workspace", need, true);
+  GDNQ_TRY(all.check());
   gdnq::ConvArgs a{};
   a.x = tok(x), a.grad_y = tok(grad_y), a.grad_x = tok(grad_x);
   a.w = w, a.bias = bias, a.state_in = state_in, a.grad_state_out = grad_state_out;

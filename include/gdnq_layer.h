@@ -12,7 +12,9 @@
  *     has (L H D, H D, D), what gdn_prefill takes and leaves, [B][H][L][D], has (H L D, D, L D), a
  *     slice of a projection's rows has the row's length as sl. Strides are in elements and >= 0;
  *     an input may repeat elements (stride 0), an output may not.
- *   - An output may not overlap an input or another output, except where a call says so.
+ *   - An output may not overlap an input or another output, except where a call says so. That is
+ *     refused (GDN_ERR_INVALID_ARG) where one of the two has no gaps between its elements or both
+ *     have the same strides; two arrays with gaps and different strides are the caller's to keep apart.
  *   - lens (device int32 [B], or NULL: every sequence has L tokens) gives the tokens of each
  *     sequence of a padded batch, each value taken into [0, L]. What stands in the arrays behind a
  *     sequence's end is neither read nor written.

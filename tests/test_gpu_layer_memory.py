@@ -44,3 +44,34 @@ def test_scan_state_gradient_in_place(B, L, D, lens):
     for b in range(B):
         if lens and lens[b] == 0:
             assert torch.equal(runs[1][2][b], dhT[b])
+
+
+def test_inputs_and_outputs_in_one_buffer():
+    """Slices of one buffer's rows, states and parameters side by side: nothing is shared, so nothing
+    is refused, and the results are those of arrays of their own."""
+    B, L, H, D, K = 2, 70, 2, 64, 4
+    C = H * D
+    r = torch.Generator(device="cuda")
+    r.manual_seed(5)
+    rows = torch.randn((B, L, 6, H, D), generator=r, device="cuda").bfloat16()
+    apart = rows.clone()
+    flat = torch.randn((8 * C + 2 * B * C,), generator=r, device="cuda")
+    w_conv, bias = flat[:4 * C].view(C, K), flat[4 * C:5 * C]
+    w_norm, dw = flat[5 * C:5 * C + D], flat[5 * C + D:5 * C + 2 * D]
+    h0, hT = flat[8 * C:8 * C + B * C].view(B, H, D), flat[8 * C + B * C:].view(B, H, D)
+    g = -torch.rand((B, L, H, D), generator=r, device="cuda")
+    conv, scan = gdn.make_conv_config(B, H, D, K), gdn.make_scan_config(B, H, D, scale="sqrt")
+    norm = gdn.make_norm_config(B, H, D, activation="silu")
+
+    def run(x, u, o, z, y, dx):
+        gdn.gdn_short_conv(conv, x, w_conv, u, bias=bias)
+        gdn.gdn_gated_scan(scan, u, g, o, h0=h0, hT=hT)
+        gdn.gdn_group_norm(norm, o, w_norm, y, z=z)
+        gdn.gdn_group_norm_backward(norm, o, w_norm, y, dx, dw, z=z, dz=torch.empty_like(z))
+        return [t.clone() for t in (u, o, y, dx, hT, dw)]
+
+    want = run(apart[:, :, 0].clone(), *(torch.empty_like(g, dtype=torch.bfloat16) for _ in range(2)),
+               apart[:, :, 3].clone(), *(torch.empty_like(g, dtype=torch.bfloat16) for _ in range(2)))
+    for a, b in zip(run(*(rows[:, :, i] for i in range(6))), want):
+        assert torch.equal(a, b)
+    assert torch.equal(rows[:, :, 0], apart[:, :, 0]) and torch.equal(rows[:, :, 3], apart[:, :, 3])
