@@ -51,9 +51,15 @@ def gdn_scan_hist_shape(cfg: _abi.gdn_scan_config, L: int) -> tuple:
     return (cfg.B, -(-L // _abi.GDN_SCAN_CHUNK), cfg.H, cfg.D)
 
 
+# The most tokens that the C entry points take: a longer count would reach them modulo 2^32.
+_MAX_TOKENS = 1 << 30
+
+
 def _shape(cfg, x: torch.Tensor):
     if x.dim() != 4:
         raise ValueError(f"x has {x.dim()} dimensions, expected [B][L][H][D]")
+    if x.shape[1] > _MAX_TOKENS:
+        raise ValueError(f"x has {x.shape[1]} tokens, at most 2^30 are taken")
     return (cfg.B, x.shape[1], cfg.H, cfg.D)
 
 
@@ -150,8 +156,12 @@ class _Args:
             raise GdnError(status, where)
 
 
+def _bytes(which: str, cfg, L: int) -> int:
+    return int(getattr(_abi.load(), which)(byref(cfg), L)) if 0 <= L <= _MAX_TOKENS else 0
+
+
 def gdn_gated_scan_workspace_bytes(cfg, L: int) -> int:
-    return int(_abi.load().gdn_gated_scan_workspace_bytes(byref(cfg), L))
+    return _bytes("gdn_gated_scan_workspace_bytes", cfg, L)
 
 
 def _scan_workspace(cfg, L: int) -> int:
@@ -202,7 +212,7 @@ def gdn_group_norm(cfg, x, w, y, b=None, z=None, lens=None, stream=None):
 
 
 def gdn_group_norm_backward_workspace_bytes(cfg, L: int) -> int:
-    return int(_abi.load().gdn_group_norm_backward_workspace_bytes(byref(cfg), L))
+    return _bytes("gdn_group_norm_backward_workspace_bytes", cfg, L)
 
 
 def gdn_group_norm_backward(cfg, x, w, dy, dx, dw, b=None, z=None, dz=None, db=None, lens=None,
@@ -232,7 +242,7 @@ def gdn_short_conv(cfg, x, w, y, bias=None, state_in=None, state_out=None, lens=
 
 
 def gdn_short_conv_backward_workspace_bytes(cfg, L: int) -> int:
-    return int(_abi.load().gdn_short_conv_backward_workspace_bytes(byref(cfg), L))
+    return _bytes("gdn_short_conv_backward_workspace_bytes", cfg, L)
 
 
 def gdn_short_conv_backward(cfg, x, w, dy, dx, dw, bias=None, db=None, state_in=None,
