@@ -313,14 +313,14 @@ gdn_status gdn_group_norm_backward(const gdn_norm_config* cfg, int32_t L, const 
   clear_error();
   Shape s;
   GDNQ_TRY(check_norm(cfg, L, &s));
-  if (s.H == 0) return GDN_OK;
+  if (s.H == 0 && cfg->weight == GDN_WEIGHT_CHANNEL) return GDN_OK;  // nothing is written
   if ((z == nullptr) != (grad_z == nullptr))
     return fail(GDN_ERR_INVALID_ARG, "grad_z goes with z");
   if ((bias == nullptr) != (grad_bias == nullptr))
     return fail(GDN_ERR_INVALID_ARG, "grad_bias goes with bias");
   GDNQ_TRY(need_ptr(grad_w, "grad_w", 4));
   GDNQ_TRY(check_opt(grad_bias, "grad_bias", 4));
-  if (s.B == 0 || L == 0) {
+  if (s.empty() || L == 0) {
     const size_t n = norm_params(cfg);
     GDNQ_TRY(zero(grad_w, n, stream, "gdn_group_norm_backward"));
     return zero(grad_bias, n, stream, "gdn_group_norm_backward");

@@ -75,3 +75,18 @@ def test_inputs_and_outputs_in_one_buffer():
     for a, b in zip(run(*(rows[:, :, i] for i in range(6))), want):
         assert torch.equal(a, b)
     assert torch.equal(rows[:, :, 0], apart[:, :, 0]) and torch.equal(rows[:, :, 3], apart[:, :, 3])
+
+
+@pytest.mark.parametrize("B,L,H", [(2, 5, 0), (0, 5, 3), (2, 0, 3)])
+def test_norm_gradients_of_an_empty_batch(B, L, H):
+    """Weights that the heads share have a gradient of zero where there is no head, as where there is no
+    sequence or token."""
+    cfg = gdn.make_norm_config(B, H, 8, act="f32")
+    e, w = torch.zeros((B, L, H, 8), device="cuda"), torch.ones(8, device="cuda")
+    dw, db = torch.full_like(w, 777.0), torch.full_like(w, 777.0)
+    gdn.gdn_group_norm_backward(cfg, e, w, e.clone(), e.clone(), dw, b=w.clone(), db=db)
+    assert float(dw.abs().max()) == 0.0 and float(db.abs().max()) == 0.0
+    per_channel = gdn.make_norm_config(B, H, 8, weight="channel", act="f32")
+    w, dw = (torch.full((H, 8), 777.0, device="cuda") for _ in range(2))
+    gdn.gdn_group_norm_backward(per_channel, e, w, e.clone(), e.clone(), dw)
+    assert float(dw.abs().sum()) == 0.0
