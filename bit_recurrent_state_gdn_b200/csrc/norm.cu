@@ -47,9 +47,11 @@ size_t norm_backward_workspace(const gdn_norm_config& cfg, int L) {
   int64_t most = (int64_t)norm_wide_parts(tokens, cfg.H) * cfg.H;
   if (cfg.D <= kNormWarp) {
     const int elem = cfg.act_dtype == GDN_DTYPE_F32 ? 4 : 2;
-    for (int lanes = 2; lanes <= 32; lanes *= 2)
-      most = std::max(most, norm_partials(norm_plan(cfg.D, cfg.H, tokens, elem, lanes, 2), cfg.H,
-                                          per_channel));
+    // for either number of CTAs per SM: fewer of them may take more parts (shares is not monotonic)
+    for (const int resident : {norm_resident(8, true), norm_resident(16, true)})
+      for (int lanes = 2; lanes <= 32; lanes *= 2)
+        most = std::max(most, norm_partials(norm_plan(cfg.D, cfg.H, tokens, elem, lanes, resident), cfg.H,
+                                            per_channel));
   }
   return (size_t)most * 2 * (size_t)cfg.D * sizeof(float);
 }
