@@ -422,7 +422,6 @@ __global__ void __launch_bounds__(kConvThreads, MINB) conv_backward_kernel(ConvA
           F2 dy[P], g[P];
           rows.get(0, u, win[u]);
           rows.get(1, u, dy);
-          const float mine = t + u < t1 ? 1.0f : 0.0f;  // dp behind the run is another run's
 #pragma unroll
           for (int e = 0; e < P; ++e) {
             F2 p = bias[e];
@@ -431,14 +430,18 @@ __global__ void __launch_bounds__(kConvThreads, MINB) conv_backward_kernel(ConvA
             F2 v, slope;
             act_pair<SILU ? GDN_ACT_SILU : GDN_ACT_NONE, true>(p, v, slope);
             dp[u][e] = f2_mul(dy[e], slope);
-            const F2 own = kInside ? dp[u][e] : f2_mul(dp[u][e], f2_all(mine));
-            db[e] = f2_add(db[e], own);
-#pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][e] = f2_fma(own, win[(u + 1 + j) % K][e], dw[j][e]);
             // token t + u - j has dp[(u - j) mod K]
             g[e] = f2_mul(w[0][e], dp[u][e]);
 #pragma unroll
             for (int j = 1; j < K; ++j) g[e] = f2_fma(w[j][e], dp[(u + K - j) % K][e], g[e]);
+          }
+          if (kInside || t + u < t1) {  // dp behind the run is another run's, or none's
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              db[e] = f2_add(db[e], dp[u][e]);
+#pragma unroll
+              for (int j = 0; j < K; ++j) dw[j][e] = f2_fma(dp[u][e], win[(u + 1 + j) % K][e], dw[j][e]);
+            }
           }
           if constexpr (kInside) {
             Vec<Act, V>::put(gx, g);

@@ -159,3 +159,29 @@ def test_conv_sums(case, ragged):
     assert torch.equal(dx.cpu()[m].double(), rx[0].view(B, L, H, D)[m])
     assert torch.equal(dw.cpu().double(), rw[0]) and torch.equal(db.cpu().double(), rb[0])
     assert torch.equal(dsi.cpu().double(), rs[0])
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (33, "f32"), (50, "bf16")])
+@pytest.mark.parametrize("L,lens", [(3, None), (70, None), (70, [70, 37]), (5000, None)])
+def test_conv_gradient_of_what_is_not_finite(L, lens, D, dtype):
+    """An infinite input meets the taps that it has in its own sequence, no others: the last token of a
+    sequence only the last tap, at any place in the middle every tap."""
+    B, K, dt = 2, 4, DT[dtype]
+    r = rng(L)
+    x, dy = (torch.randint(1, 4, (B, L, 1, D), generator=r, device="cuda").to(dt) for _ in range(2))
+    n = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    w = whole(r, (D, K), 2)
+    cfg = gdn.make_conv_config(B, 1, D, K, activation="none", act=dtype)
+    ends = [L] * B if lens is None else lens
+    want = torch.zeros((D, K), dtype=torch.float64, device="cuda")
+    x[0, ends[0] - 1, 0, 1] = x[1, ends[1] - 1, 0, 2] = math.inf
+    if L > 64:
+        for t in range(28, 37):  # around the ends of runs
+            x[0, t, 0, t - 20] = math.inf
+    for b, e in enumerate(ends):
+        xs, ds = x[b, :e, 0].double(), dy[b, :e, 0].double()
+        for j in range(K):
+            want[:, j] += (xs[:e - (K - 1 - j)] * ds[K - 1 - j:]).sum(0) if e > K - 1 - j else 0.0
+    dx, dw = torch.zeros_like(x), torch.zeros_like(w)
+    gdn.gdn_short_conv_backward(cfg, x, w, dy, dx, dw, lens=n)
+    assert torch.equal(dw.double(), want)
