@@ -10,7 +10,7 @@
 // Bound by HBM, and by latency at the two CTAs per SM that the windows' registers leave: rows come
 // K at a time through a ring in shared memory, in slots of the thread's own (no barrier in the
 // loop). bf16, K = 4, of 6452 GB/s: forward 8 x 4096 channels x 4096 tokens 97 us, 5.5 TB/s;
-// backward 4 sequences 91 us, 4.4 TB/s; one token of 1024 sequences 16 us, 4.1 TB/s.
+// backward 4 sequences 89 us, 4.5 TB/s; one token of 1024 sequences 16 us, 4.1 TB/s.
 #pragma once
 
 #include <type_traits>

@@ -58,6 +58,8 @@ struct ConvArgs {
   int activation;
 };
 
+// The SMs that work is shared out over: a constant, since the sizes of workspaces follow from it and
+// are answered on the host, whatever device is current then.
 constexpr int kSms = 148;
 
 // Into how many parts each of `units` equal pieces of work goes on a machine that holds `slots`

@@ -13,8 +13,9 @@
 //
 // Bound by HBM, and close to it by instructions: rows come through a ring in shared memory, S rows
 // ahead, each lane copying the pieces that it will read (no barrier in the loop). bf16, rows of 128
-// with a gate, of 6452 GB/s: forward 8 x 32 x 4096 tokens 138 us, 5.9 TB/s (24 instructions per
-// element); backward 4 x 32 x 4096 119 us, 5.6 TB/s (38).
+// with a gate, of 6452 GB/s: forward 8 x 32 x 4096 tokens 136 us, 5.9 TB/s (24 instructions per
+// element); backward 4 x 32 x 4096 119 us, 5.6 TB/s (38); in long runs over changing inputs, which the
+// power limit slows down, the forward pass takes 148 us.
 #pragma once
 
 #include <type_traits>
@@ -27,7 +28,7 @@ constexpr int kNormThreads = 256;
 
 // How rows are shared out over a launch; made by norm_plan.
 struct NormSplit {
-  int lanes, hb_log, heads_of_blocks, parts;  // blocks of HB heads; CTAs per block of heads
+  int hb_log, heads_of_blocks, parts;  // blocks of HB heads; CTAs per block of heads
 };
 
 // act(u) and act'(u).

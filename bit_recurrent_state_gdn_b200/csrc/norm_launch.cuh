@@ -13,7 +13,6 @@ namespace gdnq {
 // them.
 inline NormSplit norm_plan(int D, int H, int64_t tokens, int elem, int lanes, int resident) {
   NormSplit s;
-  s.lanes = lanes;
   const int rows = kNormThreads / lanes;
   int hb = 1, log = 0;
   while (hb * 2 <= rows && ((H % (hb * 2) == 0 && hb * D * elem < 512) ||
@@ -26,8 +25,15 @@ inline NormSplit norm_plan(int D, int H, int64_t tokens, int elem, int lanes, in
   return s;
 }
 
-constexpr int kNormWarp = 1024;  // channels of a head that a warp may hold
+// Channels of a head that a warp may hold. 4 x 4096 tokens, gated bf16 rows, forward / backward: 12
+// rows of 640 a token 212 / 432 us (a CTA a row: 578 / 828), 8 rows of 1024 135 / 312 (419 / 564), in
+// fp32 255 / 485 (394 / 545). Only few rows are served sooner by a CTA each: 512 of 1024 channels
+// 14.3 / 20.2 (8.0 / 12.3).
+constexpr int kNormWarp = 1024;
 
+// CTAs of the kernels for rows of more channels: eight an SM. 32768 gated bf16 rows, with 4 / 8 / 16 an
+// SM: of 2048 channels forward 190 / 182 / 158 us, backward 326 / 269 / 272; of 4096 304 / 300 / 296 and
+// 820 / 826 / 849. 4096 fp32 rows of 4096, whose partial sums count, backward 96 / 107 / 130.
 inline int norm_wide_parts(int64_t tokens, int H) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(tokens, kSms * 8 / std::max(H, 1)));
 }
@@ -68,7 +74,10 @@ cudaError_t norm_go(const NormArgs& a, cudaStream_t st) {
   }
 }
 
-// Rows of the ring by the bytes of each array that a lane holds of a row.
+// Rows of the ring by the bytes of each array that a lane holds of a row. Half as many / these / half as
+// many again, 32768 tokens of 4096 channels, gated bf16: rows of 32 (16 bytes) forward 153 / 134 / 148
+// us, backward 257 / 224 / 243; of 128 153 / 138 / 138 and 256 / 243 / 240; of 512 (32 bytes)
+// 134 / 146 / 153 and 255 / 238 / 244; of 1024 (64 bytes) 139 / 136 / 131 and 308 / 306 / 318.
 constexpr int norm_stages(int bytes, bool backward) {
   return bytes <= 4 ? 8 : bytes <= 8 ? 6 : bytes <= 16 ? 4 : bytes <= 32 ? (backward ? 3 : 4)
                     : bytes <= 64 ? (backward ? 2 : 3) : 2;
