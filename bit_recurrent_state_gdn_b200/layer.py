@@ -171,7 +171,8 @@ def _scan_workspace(cfg, L: int) -> int:
 
 def gdn_gated_scan(cfg, x, g, o, h0=None, hT=None, hist=None, lens=None, workspace=None,
                    stream=None):
-    """x, o act [B][L][H][D]; g fp32 [B][L][H][D], the log of the gate; h0, hT fp32 [B][H][D];
+    """x, o act [B][L][H][D]; g fp32 [B][L][H][D], the log of the gate; h0, hT fp32 [B][H][D] (may
+    be the same);
     hist fp32 of gdn_scan_hist_shape(cfg, L), for the backward pass; lens int32 [B]. workspace: at
     least gdn_gated_scan_workspace_bytes(cfg, L) bytes on the device, made here when None."""
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
@@ -187,7 +188,7 @@ def gdn_gated_scan(cfg, x, g, o, h0=None, hT=None, hist=None, lens=None, workspa
 def gdn_gated_scan_backward(cfg, x, g, hist, do, dx, dg, dhT=None, dh0=None, lens=None,
                             workspace=None, stream=None):
     """x, g, lens of the forward call and the hist that it wrote; do, dx act [B][L][H][D]; dg fp32
-    [B][L][H][D]; dhT, dh0 fp32 [B][H][D]; workspace as in the forward call."""
+    [B][L][H][D]; dhT, dh0 fp32 [B][H][D] (may be the same); workspace as in the forward call."""
     a, act = _Args(cfg, x), _TORCH_DT[cfg.act_dtype]
     n = cfg.B * cfg.H * cfg.D
     f32, L = torch.float32, a.shape[1]
